@@ -15,6 +15,7 @@ error status, a ``QSError`` is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -26,7 +27,8 @@ QS_FLAG_NO_ROTATE = 1
 QS_FLAG_BYTE_CODES = 2
 QS_MAX_K = 65536
 STATUS = {0: "QS_OK", 1: "QS_ERR_NULL", 2: "QS_ERR_SHAPE", 3: "QS_ERR_BITS", 4: "QS_ERR_ALIGN",
-          5: "QS_ERR_RANGE", 6: "QS_ERR_CUDA", 7: "QS_ERR_TIMEOUT", 8: "QS_ERR_PTR"}
+          5: "QS_ERR_RANGE", 6: "QS_ERR_CUDA", 7: "QS_ERR_TIMEOUT", 8: "QS_ERR_PTR",
+          9: "QS_ERR_DTYPE"}
 EXPORTS = ("qs_pack_weights", "qs_quant_act", "qs_qlinear", "qs_qlinear_mixed", "qs_qgemm_s32",
            "qs_qgemm_s32_mixed", "qs_gelu_bf16", "qs_linear_workspace_bytes", "qs_linear",
            "qs_linear_mixed", "qs_linear_ex", "qs_linear_noalloc", "qs_pack_weights_bgr",
@@ -36,12 +38,24 @@ EXPORTS = ("qs_pack_weights", "qs_quant_act", "qs_qlinear", "qs_qlinear_mixed", 
            "qs_sd4_linear_e4m3w", "qs_sd4_linear_e4m3", "qs_sd4_scale_tiles_bytes",
            "qs_sd4_scale_tiles", "qs_sd4_linear_e4m3_tiles", "qs_sd4_quant_decomp",
            "qs_sd4_linear_decomp", "qs_gbs_reset", "qs_gbs_update", "qs_linear_gbs",
-           "qs_selftest_timeout", "qs_device_error", "qs_status_str", "qs_version")
+           "qs_selftest_timeout", "qs_device_error", "qs_status_str", "qs_version", "qs_rope",
+           "qs_lora_workspace_bytes", "qs_lora_add", "qs_block_means", "qs_block_select",
+           "qs_block_attention_workspace_bytes", "qs_block_attention")
+QS_ROPE_INTERLEAVED, QS_ROPE_INVERSE = 1, 2
+QS_ATTN_CAUSAL = 1
+QS_BLOCK_Q, QS_BLOCK_K = 128, 64
+QS_BF16, QS_F16, QS_F32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: QS_BF16, torch.float16: QS_F16, torch.float32: QS_F32}
 BITS = (4, 6, 8)
 QS_GBS_MAX_BLOCKS = 1024
 # sizeof(qs_gbs_state): acc, last_d (f64), bits, step, blocks_done, reserved (i32), partials
 QS_GBS_STATE_BYTES = 8 + 8 + 4 * 4 + 2 * QS_GBS_MAX_BLOCKS * 8
 QS_NOALLOC_SCRATCH_BYTES = 8 << 20
+
+
+class _Strides(ctypes.Structure):
+    """qs_strides: strides of a [batch, row, head, dim] view in elements."""
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 class QSError(RuntimeError):
@@ -101,6 +115,20 @@ def load() -> ctypes.CDLL:
     L.qs_gbs_reset.argtypes = [vp, vp]
     L.qs_gbs_update.argtypes = [vp, vp, i64, f64, vp, vp]
     L.qs_linear_gbs.argtypes = [vp, i64, i64, f32, vp, vp, vp, vp, vp, i64, vp, vp, i64, vp, vp]
+    st = ctypes.POINTER(_Strides)
+    L.qs_rope.argtypes = [vp, i64, i64, i64, i64, i64, i64, vp, i32, vp, vp, f64, u32, i32, vp, i64,
+                          i64, vp]
+    L.qs_lora_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.qs_lora_workspace_bytes.restype = i64
+    L.qs_lora_add.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, i64, i64, vp, vp, i64, vp, i64, vp,
+                              vp]
+    L.qs_block_means.argtypes = [vp, st, i64, i64, i64, i64, i32, vp, i64, vp, vp]
+    L.qs_block_select.argtypes = [vp, st, i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64,
+                                  i64, u32, vp, vp]
+    L.qs_block_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    L.qs_block_attention_workspace_bytes.restype = i64
+    L.qs_block_attention.argtypes = [vp, st, vp, st, vp, st, i64, i64, i64, i64, i64, i64, i32, vp,
+                                     i64, vp, vp, f32, u32, vp, i64, vp, st, vp, vp]
     L.qs_selftest_timeout.argtypes = [i64, vp]
     L.qs_device_error.argtypes = [vp]
     L.qs_status_str.argtypes = [i32]
@@ -115,7 +143,8 @@ def load() -> ctypes.CDLL:
                  "qs_sd4_linear_e4m3", "qs_sd4_scale_tiles", "qs_sd4_linear_e4m3_tiles",
                  "qs_sd4_quant_decomp", "qs_sd4_linear_decomp",
                  "qs_gbs_reset", "qs_gbs_update", "qs_linear_gbs", "qs_selftest_timeout",
-                 "qs_device_error"):
+                 "qs_device_error", "qs_rope", "qs_lora_add", "qs_block_means", "qs_block_select",
+                 "qs_block_attention"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -549,6 +578,131 @@ def qs_linear_gbs(x, M, K, alpha, w4_packed, w4_scale, w8_packed, w8_scale, bias
            "qs_linear_gbs")
 
 
+def _view(t, name, dtypes=(torch.bfloat16, torch.float16), dims=4):
+    """A CUDA view of `dims` dimensions whose last one is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _strides(t):
+    return ctypes.byref(_Strides(t.stride(0), t.stride(1), t.stride(2)))
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def qs_rope(x, positions, inv_freq, y, pair_axis=None, scale=1.0, flags=0, stream=None):
+    """x, y: [rows, heads, head_dim] views (y may be x); sizes and strides are theirs."""
+    _view(x, "x", tuple(_DTYPES), 3)
+    _view(y, "y", (x.dtype,), 3)
+    _shape(y, x.shape, "y")
+    _cuda(positions, torch.int64, "positions")
+    _cuda(inv_freq, torch.float64, "inv_freq")
+    _cuda(pair_axis, torch.int32, "pair_axis")
+    rows, heads, dim = x.shape
+    if positions.dim() not in (1, 2) or positions.shape[0] != rows:
+        raise ValueError("positions must be [rows] or [rows, axes]")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    _shape(pair_axis, inv_freq.shape, "pair_axis")
+    _check(load().qs_rope(_p(x), x.stride(0), x.stride(1), rows, heads, dim, 2 * inv_freq.numel(),
+                          _p(positions), positions.shape[1] if positions.dim() == 2 else 1,
+                          _p(pair_axis), _p(inv_freq), float(scale), flags, _DTYPES[x.dtype], _p(y),
+                          y.stride(0), y.stride(1), _s(stream)), "qs_rope")
+
+
+def qs_lora_workspace_bytes(M, K, R, requests) -> int:
+    return int(load().qs_lora_workspace_bytes(M, K, R, requests))
+
+
+def qs_lora_add(x, y, M, K, N, a, b, scale, adapters, R, seg_start, seg_adapter, requests,
+                workspace, workspace_bytes, out, stream=None):
+    for t, name in ((x, "x"), (y, "y"), (a, "a"), (b, "b"), (out, "out")):
+        _cuda(t, torch.bfloat16, name)
+    _cuda(scale, torch.float32, "scale")
+    _cuda(seg_start, torch.int32, "seg_start")
+    _cuda(seg_adapter, torch.int32, "seg_adapter")
+    _cuda(workspace, torch.uint8, "workspace")
+    _check(load().qs_lora_add(_p(x), _p(y), M, K, N, _p(a), _p(b), _p(scale), adapters, R,
+                              _p(seg_start), _p(seg_adapter), requests, _p(workspace),
+                              workspace_bytes, _p(out), _s(stream)), "qs_lora_add")
+
+
+def qs_block_means(x, lens, first_block, means, stream=None):
+    """x: [B, L, H, D] view; means: float32 [B, H, ceil(L / 64), D]."""
+    _view(x, "x")
+    B, L, H, D = x.shape
+    _cuda(means, torch.float32, "means")
+    _shape(means, (B, H, -(-L // QS_BLOCK_K), D), "means")
+    _cuda(lens, torch.int32, "lens")
+    _shape(lens, (B,), "lens")
+    _check(load().qs_block_means(_p(x), _strides(x), B, L, H, D, _DTYPES[x.dtype], _p(lens),
+                                 first_block, _p(means), _s(stream)), "qs_block_means")
+
+
+def qs_block_select(q, means, Lk, q_len, k_len, T, keep_first, keep_last, flags, blocks,
+                    stream=None):
+    """q: [B, Lq, Hq, D] view; means: float32 [B, Hkv, ceil(Lk / 64), D]; blocks: int32
+    [B, Hq, ceil(Lq / 128), T]."""
+    _view(q, "q")
+    B, Lq, Hq, D = q.shape
+    _cuda(means, torch.float32, "means")
+    if means.dim() != 4:
+        raise ValueError("means must be [B, Hkv, blocks, D]")
+    Hkv = means.shape[1]
+    _shape(means, (B, Hkv, -(-Lk // QS_BLOCK_K), D), "means")
+    _cuda(blocks, torch.int32, "blocks")
+    _shape(blocks, (B, Hq, -(-Lq // QS_BLOCK_Q), T), "blocks")
+    for t, name in ((q_len, "q_len"), (k_len, "k_len")):
+        _cuda(t, torch.int32, name)
+        _shape(t, (B,), name)
+    _check(load().qs_block_select(_p(q), _strides(q), B, Lq, Hq, D, _DTYPES[q.dtype], _p(means), Lk,
+                                  Hkv, _p(q_len), _p(k_len), T, keep_first, keep_last, flags,
+                                  _p(blocks), _s(stream)), "qs_block_select")
+
+
+def qs_block_attention_workspace_bytes(B, Lq, Hq, D, T) -> int:
+    return int(load().qs_block_attention_workspace_bytes(B, Lq, Hq, D, T))
+
+
+def qs_block_attention(q, k, v, blocks, q_len, k_len, scale, flags, workspace, out, lse,
+                       stream=None):
+    """q, out: [B, Lq, Hq, D], k, v: [B, Lk, Hkv, D] views; blocks: int32
+    [B, Hq, ceil(Lq / 128), T]; lse: float32 [B, Hq, Lq] or None."""
+    _view(q, "q")
+    B, Lq, Hq, D = q.shape
+    for t, name in ((k, "k"), (v, "v"), (out, "out")):
+        _view(t, name, (q.dtype,))
+    _, Lk, Hkv, _ = k.shape
+    _shape(k, (B, Lk, Hkv, D), "k")
+    _shape(v, k.shape, "v")
+    _shape(out, q.shape, "out")
+    _cuda(blocks, torch.int32, "blocks")
+    if blocks.dim() != 4:
+        raise ValueError("blocks must be [B, Hq, query blocks, T]")
+    T = blocks.shape[3]
+    _shape(blocks, (B, Hq, -(-Lq // QS_BLOCK_Q), T), "blocks")
+    for t, name in ((q_len, "q_len"), (k_len, "k_len")):
+        _cuda(t, torch.int32, name)
+        _shape(t, (B,), name)
+    _cuda(workspace, torch.uint8, "workspace")
+    _cuda(lse, torch.float32, "lse")
+    _shape(lse, (B, Hq, Lq), "lse")
+    _check(load().qs_block_attention(_p(q), _strides(q), _p(k), _strides(k), _p(v), _strides(v), B,
+                                     Lq, Lk, Hq, Hkv, D, _DTYPES[q.dtype], _p(blocks), T,
+                                     _p(q_len), _p(k_len), float(scale), flags, _p(workspace),
+                                     0 if workspace is None else workspace.numel(), _p(out),
+                                     _strides(out), _p(lse), _s(stream)), "qs_block_attention")
+
+
 def qs_selftest_timeout(timeout_us: int, stream=None) -> None:
     _check(load().qs_selftest_timeout(timeout_us, _s(stream)), "qs_selftest_timeout")
 
@@ -675,6 +829,165 @@ def linear(x, w_packed, w_scale, bias, bits: int, alpha: float = 1.0, workspace=
     return out
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a kernel on `stream` (None: the current one), allocated on that stream: memory
+    that is freed while the kernel runs then goes to later work of the same stream only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, axes=None, scaling: str | None = None,
+                     factor: float = 1.0, trained_length: int = 4096, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cuda"):
+    """Frequencies for `rope`: (inv_freq float64 [rot_dim/2], pair_axis int32 [rot_dim/2] or None,
+    scale).
+
+    axes     sizes of the sections of a head that turn with each position axis (they sum to
+             rot_dim; a video's time, height, width): section of size s has the frequencies
+             theta^(-2i/s)
+    scaling  how positions beyond `trained_length` are handled (one axis):
+             "linear"  all frequencies divided by `factor`
+             "ntk"     theta raised to theta * factor^(d/(d-2)): the slowest pair is divided by
+                       factor, the fastest stays
+             "yarn"    pairs that turn more than beta_fast times over the trained length stay,
+                       those below beta_slow turns are divided by factor, a linear ramp between;
+                       scale = 0.1 ln(factor) + 1
+    """
+    sizes = [rot_dim] if axes is None else list(axes)
+    if rot_dim < 2 or any(s < 2 or s % 2 for s in sizes) or sum(sizes) != rot_dim:
+        raise ValueError("rot_dim and the axes' sizes are even, and the sizes sum to rot_dim")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn'")
+    if scaling is not None and (len(sizes) > 1 or factor < 1.0):
+        raise ValueError("scaling takes one axis and a factor of at least 1")
+    scale = 1.0
+    if scaling == "ntk" and rot_dim > 2:
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    inv = torch.cat([theta ** (-torch.arange(0, s, 2, dtype=torch.float64) / s) for s in sizes])
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        # the (fractional) pair that makes `turns` full turns over the trained length
+        def pair(turns):
+            return rot_dim * math.log(trained_length / (turns * 2 * math.pi)) / (2 * math.log(theta))
+
+        lo = max(math.floor(pair(beta_fast)), 0)
+        hi = min(math.ceil(pair(beta_slow)), rot_dim - 1)
+        ramp = (torch.arange(rot_dim // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)
+        ramp = ramp.clamp(0, 1)
+        inv = inv * (1 - ramp) + inv / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    axis = None
+    if len(sizes) > 1:
+        axis = torch.cat([torch.full((s // 2,), i, dtype=torch.int32) for i, s in enumerate(sizes)])
+        axis = axis.to(device)
+    return inv.to(device), axis, scale
+
+
+def rope(x, positions, inv_freq, pair_axis=None, interleaved: bool = True, scale: float = 1.0,
+         inverse: bool = False, out=None, stream=None):
+    """Rotary positions on x [rows, heads, head_dim] (bf16, fp16 or fp32; a view such as the query
+    and key columns of a qkv projection's output): ``positions`` int64 [rows] or [rows, axes],
+    ``inv_freq`` float64 [rot_dim/2] and ``pair_axis`` (`rope_frequencies`).  ``out`` may be x (in
+    place); by default a new contiguous tensor."""
+    if out is None:
+        _view(x, "x", tuple(_DTYPES), 3)
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    flags = (QS_ROPE_INTERLEAVED if interleaved else 0) | (QS_ROPE_INVERSE if inverse else 0)
+    qs_rope(x, positions, inv_freq, out, pair_axis, scale, flags, stream)
+    return out
+
+
+def lora_add(y, x, a, b, seg_start, seg_adapter, scale=None, out=None, workspace=None, stream=None):
+    """y + scale_i * (x A_i^T) B_i^T with i the adapter of each row's request: y bf16 [M, N] (a
+    projection's output), x bf16 [M, K], a bf16 [adapters, R, K], b bf16 [adapters, N, R],
+    ``seg_start`` int32 [requests + 1], ``seg_adapter`` int32 [requests] (-1: none).  In place
+    unless ``out`` is given; rows outside every request are left as they were."""
+    M, K = x.shape
+    adapters, R, _ = a.shape
+    N, requests = y.shape[1], seg_adapter.shape[0]
+    out = y if out is None else out
+    for t, name, shape in ((y, "y", (M, N)), (a, "a", (adapters, R, K)), (b, "b", (adapters, N, R)),
+                           (out, "out", (M, N)), (scale, "scale", (adapters,)),
+                           (seg_start, "seg_start", (requests + 1,)),
+                           (seg_adapter, "seg_adapter", (requests,))):
+        _shape(t, shape, name)
+    if workspace is None:
+        need = qs_lora_workspace_bytes(M, K, R, requests)
+        if need < 0:
+            raise QSError(2, f"qs_lora_workspace_bytes({M}, {K}, {R}, {requests})")
+        workspace = _empty((need,), torch.uint8, x.device, stream)
+    qs_lora_add(x, y, M, K, N, a, b, scale, adapters, R, seg_start, seg_adapter, requests,
+                workspace, workspace.numel(), out, stream)
+    return out
+
+
+def block_means(x, lens=None, first_block: int = 0, out=None, stream=None):
+    """Means of the 64-row blocks of x [B, L, H, D] (keys): float32 [B, H, ceil(L / 64), D].  With
+    ``out`` and ``first_block`` only the blocks from that one on are formed (a cache that grew)."""
+    _view(x, "x")
+    B, L, H, D = x.shape
+    if out is None:
+        if first_block:
+            raise ValueError("first_block needs the means so far (out)")
+        out = _empty((B, H, -(-L // QS_BLOCK_K), D), torch.float32, x.device, stream)
+    qs_block_means(x, lens, first_block, out, stream)
+    return out
+
+
+def block_select(q, means, count: int, keys: int, first: int = 0, last: int = 0,
+                 causal: bool = False, q_len=None, k_len=None, out=None, stream=None):
+    """The ``count`` key blocks that each block of 128 queries of q [B, Lq, Hq, D] attends to, by
+    the product of block means (``means`` from `block_means` of ``keys`` keys): int32
+    [B, Hq, ceil(Lq / 128), count], ascending, -1 behind the last.  The ``first`` and ``last``
+    visible blocks are always among them."""
+    _view(q, "q")
+    B, Lq, Hq, _ = q.shape
+    if out is None:
+        out = _empty((B, Hq, -(-Lq // QS_BLOCK_Q), count), torch.int32, q.device, stream)
+    qs_block_select(q, means, keys, q_len, k_len, count, first, last,
+                    QS_ATTN_CAUSAL if causal else 0, out, stream)
+    return out
+
+
+def block_attention(q, k, v, blocks, scale: float | None = None, causal: bool = False, q_len=None,
+                    k_len=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of q [B, Lq, Hq, D] over the listed 64-key blocks of k, v [B, Lk, Hkv, D] (bf16 or
+    fp16, D 64 or 128): (out, lse float32 [B, Hq, Lq]).  ``blocks`` as from `block_select`;
+    ``scale`` defaults to D^-1/2.  Rows at and behind ``q_len`` keep what ``out`` and ``lse`` held."""
+    _view(q, "q")
+    B, Lq, Hq, D = q.shape
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    if lse is None:
+        lse = _empty((B, Hq, Lq), torch.float32, q.device, stream)
+    if workspace is None:
+        need = qs_block_attention_workspace_bytes(B, Lq, Hq, D, blocks.shape[-1])
+        if need > 0:
+            workspace = _empty((need,), torch.uint8, q.device, stream)
+    qs_block_attention(q, k, v, blocks, q_len, k_len, D ** -0.5 if scale is None else scale,
+                       QS_ATTN_CAUSAL if causal else 0, workspace, out, lse, stream)
+    return out, lse
+
+
+class LoraBatch:
+    """The adapters of one batch beside a projection: stacked factors a [adapters, R, K] and
+    b [adapters, N, R], a scale for each, and which rows belong to which request (`lora_add`)."""
+
+    def __init__(self, a, b, seg_start, seg_adapter, scale=None):
+        self.a, self.b, self.scale = a, b, scale
+        self.seg_start, self.seg_adapter = seg_start, seg_adapter
+
+    def add(self, y, x, stream=None):
+        return lora_add(y, x, self.a, self.b, self.seg_start, self.seg_adapter, self.scale,
+                        stream=stream)
+
+
 class QuantLinear:
     """A Hadamard-rotated quantized linear layer (W4A4, W8A8, or mixed such as
     W4A8 / W4A6 with ``bits_x``): weights packed once; each call runs the
@@ -683,7 +996,8 @@ class QuantLinear:
     codes two per byte ("packed", packed int4 widened in the GEMM's shared
     memory; the faster form with the GEMM's 256 x 512 tiles) or one per byte
     ("bytes", loaded by TMA straight into the operand tiles); the codes, and
-    so the outputs, are the same."""
+    so the outputs, are the same.  ``lora`` adds the batch's low-rank adapters
+    to the output of a call."""
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None, bits: int,
                  alpha: float = 1.0, bits_x: int | None = None, act_codes: str = "packed"):
@@ -698,13 +1012,13 @@ class QuantLinear:
         self.bias = bias
         self.workspace = None
 
-    def __call__(self, x: torch.Tensor, stream=None, out=None) -> torch.Tensor:
+    def __call__(self, x: torch.Tensor, stream=None, out=None, lora: LoraBatch | None = None) -> torch.Tensor:
         need = qs_linear_workspace_bytes(x.shape[0], self.K, storage_bits(self.bits_x, self.x_flags))
         if self.workspace is None or self.workspace.numel() < need:
             self.workspace = torch.empty((max(need, 0),), dtype=torch.uint8, device=x.device)
-        return linear(x, self.w_packed, self.w_scale, self.bias, self.bits_x, self.alpha,
-                      self.workspace, stream=stream, out=out, bits_w=self.bits,
-                      x_flags=self.x_flags)
+        y = linear(x, self.w_packed, self.w_scale, self.bias, self.bits_x, self.alpha,
+                   self.workspace, stream=stream, out=out, bits_w=self.bits, x_flags=self.x_flags)
+        return y if lora is None else lora.add(y, x, stream)
 
 
 def gbs_state_host(state) -> dict:

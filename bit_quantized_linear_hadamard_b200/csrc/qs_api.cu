@@ -11,14 +11,18 @@
 #include <mutex>
 
 #include "qs.h"
+#include "qs_attn.cuh"
 #include "qs_bgr.cuh"
 #include "qs_gbs.cuh"
 #include "qs_gemm.cuh"
 #include "qs_host.cuh"
 #include "qs_glue.cuh"
+#include "qs_lora.cuh"
 #include "qs_quant.cuh"
+#include "qs_rope.cuh"
 #include "qs_sd4.cuh"
 #include "qs_sd4_mx.cuh"
+#include "qs_select.cuh"
 
 namespace {
 
@@ -243,6 +247,33 @@ qs_status launch_sd4_quant_tc(const void* x, int64_t rows, int64_t K, void* out,
                                               static_cast<int>(K), static_cast<uint8_t*>(out), meta);
   return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A [B, L, H, D] view of 16-bit elements that 16-byte accesses and tensor maps can take.
+qs_status check_view(const void* p, const qs_strides* st, int64_t B, int64_t L, int64_t H,
+                     int64_t D, int dtype) {
+  if (!p || !st) return QS_ERR_NULL;
+  if (dtype != QS_BF16 && dtype != QS_F16) return QS_ERR_DTYPE;
+  if (B <= 0 || L <= 0 || H <= 0 || (D != 64 && D != 128)) return QS_ERR_SHAPE;
+  if (B > 65535 || H > 65535 || L > QS_MAX_LEN) return QS_ERR_RANGE;
+  if (!aligned16(p)) return QS_ERR_ALIGN;
+  const int64_t size[3] = {B, L, H}, stride[3] = {st->batch, st->row, st->head};
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
+    if (stride[i] < 0 || (i == 1 && stride[i] == 0)) return QS_ERR_SHAPE;
+    if (stride[i] >= (1LL << 39)) return QS_ERR_RANGE;
+    if (stride[i] % 8 != 0) return QS_ERR_ALIGN;
+  }
+  return check_device_ptr(p);
+}
+
+qs_status check_ints(const int32_t* p) {
+  if (!p) return QS_OK;
+  return aligned_to(p, 4) ? check_device_ptr(p) : QS_ERR_ALIGN;
+}
+
+qs::select::Strides select_strides(const qs_strides* st) { return {st->batch, st->row, st->head}; }
 
 }  // namespace
 
@@ -869,6 +900,228 @@ qs_status qs_gelu_bf16(const void* x_bf16, int64_t n, void* y_bf16, void* stream
   return cudaGetLastError() == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 
+qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, int64_t rows,
+                  int64_t heads, int64_t head_dim, int64_t rot_dim, const int64_t* positions,
+                  int axes, const int32_t* pair_axis, const double* inv_freq, double scale,
+                  unsigned flags, int dtype, void* y, int64_t y_row_stride, int64_t y_head_stride,
+                  void* stream) {
+  if (!x || !y || !positions || !inv_freq) return QS_ERR_NULL;
+  if (dtype != QS_BF16 && dtype != QS_F16 && dtype != QS_F32) return QS_ERR_DTYPE;
+  if (rows <= 0 || heads <= 0 || head_dim <= 0 || rot_dim < 2 || rot_dim % 2 != 0 ||
+      rot_dim > head_dim)
+    return QS_ERR_SHAPE;
+  if (rows > QS_MAX_ROWS || heads > 65535 || head_dim > qs::rope::kMaxDim || axes < 1 || axes > 8)
+    return QS_ERR_RANGE;
+  if ((flags & ~(QS_ROPE_INTERLEAVED | QS_ROPE_INVERSE)) || !std::isfinite(scale))
+    return QS_ERR_RANGE;
+  // rows and heads of y that share elements would race
+  if (x_row_stride < 0 || x_head_stride < 0 || y_row_stride < 0 || y_head_stride < 0 ||
+      (rows > 1 && y_row_stride == 0) || (heads > 1 && y_head_stride == 0))
+    return QS_ERR_SHAPE;
+  const uintptr_t elem = dtype == QS_F32 ? 4 : 2;
+  if (!aligned_to(x, elem) || !aligned_to(y, elem) || !aligned_to(positions, 8) ||
+      !aligned_to(inv_freq, 8))
+    return QS_ERR_ALIGN;
+  QS_TRY(check_ints(pair_axis));
+  QS_TRY(check_device_ptr(x));
+  QS_TRY(check_device_ptr(y));
+  QS_TRY(check_device_ptr(positions));
+  QS_TRY(check_device_ptr(inv_freq));
+  const int sms = qs::sm_count();
+  if (sms <= 0) return QS_ERR_CUDA;
+  qs::rope::Args a{};
+  a.x = x, a.y = y;
+  a.x_row = x_row_stride, a.x_head = x_head_stride;
+  a.y_row = y_row_stride, a.y_head = y_head_stride;
+  a.rows = rows;
+  a.heads = static_cast<int>(heads), a.dim = static_cast<int>(head_dim);
+  a.pairs = static_cast<int>(rot_dim / 2), a.axes = axes;
+  a.pos = positions, a.axis = pair_axis, a.inv_freq = inv_freq, a.scale = scale;
+  a.inverse = (flags & QS_ROPE_INVERSE) != 0;
+  a.copy_tail = !(x == y && x_row_stride == y_row_stride && x_head_stride == y_head_stride);
+  const bool inter = (flags & QS_ROPE_INTERLEAVED) != 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == QS_F32   ? qs::rope::launch<float>(a, inter, sms, s)
+                        : dtype == QS_F16 ? qs::rope::launch<__half>(a, inter, sms, s)
+                                          : qs::rope::launch<__nv_bfloat16>(a, inter, sms, s);
+  return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
+int64_t qs_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t requests) {
+  if (check_rows_k(M, K) != QS_OK || R < 8 || R % 8 != 0 || R > qs::lora::kMaxRank ||
+      requests <= 0 || requests > QS_MAX_ROWS)
+    return -1;
+  return qs::lora::plan(M, K, R, requests).slices * M * R * 4;
+}
+
+qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t K, int64_t N,
+                      const void* a_bf16, const void* b_bf16, const float* scale,
+                      int64_t adapters, int64_t R, const int32_t* seg_start,
+                      const int32_t* seg_adapter, int64_t requests, void* workspace,
+                      int64_t workspace_bytes, void* out_bf16, void* stream) {
+  if (!x_bf16 || !y_bf16 || !a_bf16 || !b_bf16 || !seg_start || !seg_adapter || !workspace ||
+      !out_bf16)
+    return QS_ERR_NULL;
+  QS_TRY(check_rows_k(M, K));
+  if (N <= 0 || N % 16 != 0 || R < 8 || R % 8 != 0 || adapters <= 0 || requests <= 0)
+    return QS_ERR_SHAPE;
+  if (N > QS_MAX_ROWS || R > qs::lora::kMaxRank || adapters > QS_MAX_ROWS ||
+      requests > QS_MAX_ROWS - M)
+    return QS_ERR_RANGE;
+  const int64_t need = qs_lora_workspace_bytes(M, K, R, requests);
+  if (need < 0 || workspace_bytes < need) return QS_ERR_RANGE;
+  for (const void* p : {x_bf16, y_bf16, a_bf16, b_bf16, static_cast<const void*>(workspace),
+                        static_cast<const void*>(out_bf16)}) {
+    if (!aligned16(p)) return QS_ERR_ALIGN;
+    QS_TRY(check_device_ptr(p));
+  }
+  if (scale) {
+    if (!aligned_to(scale, 4)) return QS_ERR_ALIGN;
+    QS_TRY(check_device_ptr(scale));
+  }
+  QS_TRY(check_ints(seg_start));
+  QS_TRY(check_ints(seg_adapter));
+  qs::lora::Args a{};
+  a.x = static_cast<const uint16_t*>(x_bf16), a.y = static_cast<const uint16_t*>(y_bf16);
+  a.a = static_cast<const uint16_t*>(a_bf16), a.b = static_cast<const uint16_t*>(b_bf16);
+  a.out = static_cast<uint16_t*>(out_bf16), a.scale = scale;
+  a.start = seg_start, a.ids = seg_adapter, a.part = static_cast<float*>(workspace);
+  a.M = M, a.K = static_cast<int>(K), a.N = static_cast<int>(N), a.R = static_cast<int>(R);
+  a.adapters = static_cast<int>(adapters), a.requests = static_cast<int>(requests);
+  const qs::lora::Plan p = qs::lora::plan(M, K, R, requests);
+  a.slices = p.slices;
+  const cudaError_t e = qs::lora::launch(a, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
+qs_status qs_block_means(const void* x, const qs_strides* x_strides, int64_t B, int64_t L,
+                         int64_t H, int64_t D, int dtype, const int32_t* len,
+                         int64_t first_block, float* means, void* stream) {
+  if (!x || !x_strides || !means) return QS_ERR_NULL;
+  QS_TRY(check_view(x, x_strides, B, L, H, D, dtype));
+  const int64_t blocks = (L + QS_BLOCK_K - 1) / QS_BLOCK_K;
+  if (first_block < 0 || first_block >= blocks) return QS_ERR_RANGE;
+  if (B * H * blocks > QS_MAX_ROWS) return QS_ERR_RANGE;
+  if (!aligned16(means)) return QS_ERR_ALIGN;
+  QS_TRY(check_ints(len));
+  QS_TRY(check_device_ptr(means));
+  qs::select::MeanArgs a{};
+  a.x = static_cast<const uint16_t*>(x), a.st = select_strides(x_strides), a.len = len;
+  a.means = means, a.L = L, a.B = static_cast<int>(B), a.H = static_cast<int>(H);
+  a.blocks = static_cast<int>(blocks), a.first = static_cast<int>(first_block);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == QS_F16;
+  const cudaError_t e =
+      D == 64 ? (f16 ? qs::select::launch_means<64, true>(a, s) : qs::select::launch_means<64, false>(a, s))
+              : (f16 ? qs::select::launch_means<128, true>(a, s) : qs::select::launch_means<128, false>(a, s));
+  return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
+qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B, int64_t Lq,
+                          int64_t Hq, int64_t D, int dtype, const float* means, int64_t Lk,
+                          int64_t Hkv, const int32_t* q_len, const int32_t* k_len, int64_t T,
+                          int64_t keep_first, int64_t keep_last, unsigned flags, int32_t* blocks,
+                          void* stream) {
+  if (!q || !q_strides || !means || !blocks) return QS_ERR_NULL;
+  QS_TRY(check_view(q, q_strides, B, Lq, Hq, D, dtype));
+  if (Lk <= 0 || Hkv <= 0 || Hq % Hkv != 0 || T <= 0) return QS_ERR_SHAPE;
+  const int64_t nk = (Lk + QS_BLOCK_K - 1) / QS_BLOCK_K;
+  if (Lk > QS_MAX_LEN || nk > qs::select::kMaxBlocks || T > INT32_MAX || keep_first < 0 ||
+      keep_last < 0 || (flags & ~QS_ATTN_CAUSAL))
+    return QS_ERR_RANGE;
+  if (!aligned16(means) || !aligned_to(blocks, 4)) return QS_ERR_ALIGN;
+  QS_TRY(check_ints(q_len));
+  QS_TRY(check_ints(k_len));
+  QS_TRY(check_device_ptr(means));
+  QS_TRY(check_device_ptr(blocks));
+  qs::select::SelectArgs a{};
+  a.q = static_cast<const uint16_t*>(q), a.st = select_strides(q_strides), a.means = means;
+  a.q_len = q_len, a.k_len = k_len, a.blocks = blocks, a.Lq = Lq, a.Lk = Lk;
+  a.B = static_cast<int>(B), a.Hq = static_cast<int>(Hq), a.Hkv = static_cast<int>(Hkv);
+  a.nq = static_cast<int>((Lq + QS_BLOCK_Q - 1) / QS_BLOCK_Q), a.nk = static_cast<int>(nk);
+  a.T = static_cast<int>(T);
+  a.first = static_cast<int>(keep_first < nk ? keep_first : nk);
+  a.last = static_cast<int>(keep_last < nk ? keep_last : nk);
+  a.causal = (flags & QS_ATTN_CAUSAL) != 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == QS_F16;
+  const cudaError_t e =
+      D == 64 ? (f16 ? qs::select::launch_select<64, true>(a, s) : qs::select::launch_select<64, false>(a, s))
+              : (f16 ? qs::select::launch_select<128, true>(a, s) : qs::select::launch_select<128, false>(a, s));
+  return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
+int64_t qs_block_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t D,
+                                           int64_t T) {
+  if (B <= 0 || Lq <= 0 || Hq <= 0 || (D != 64 && D != 128) || T <= 0) return -1;
+  if (B > 65535 || Hq > 65535 || Lq > QS_MAX_LEN || T > QS_MAX_LEN) return -1;
+  const qs::attn::Plan p = qs::attn::plan(B, Hq, Lq, T);
+  return p.splits > 1 ? p.splits * B * Hq * Lq * (D + 1) * 4 : 0;
+}
+
+qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const void* k,
+                             const qs_strides* k_strides, const void* v,
+                             const qs_strides* v_strides, int64_t B, int64_t Lq, int64_t Lk,
+                             int64_t Hq, int64_t Hkv, int64_t D, int dtype,
+                             const int32_t* blocks, int64_t T, const int32_t* q_len,
+                             const int32_t* k_len, float scale, unsigned flags, void* workspace,
+                             int64_t workspace_bytes, void* out, const qs_strides* out_strides,
+                             float* lse, void* stream) {
+  if (!q || !k || !v || !q_strides || !k_strides || !v_strides || !blocks || !out || !out_strides)
+    return QS_ERR_NULL;
+  QS_TRY(check_view(q, q_strides, B, Lq, Hq, D, dtype));
+  QS_TRY(check_view(k, k_strides, B, Lk, Hkv, D, dtype));
+  QS_TRY(check_view(v, v_strides, B, Lk, Hkv, D, dtype));
+  QS_TRY(check_view(out, out_strides, B, Lq, Hq, D, dtype));
+  if (Hq % Hkv != 0 || T <= 0 || (B > 1 && out_strides->batch == 0) ||
+      (Hq > 1 && out_strides->head == 0))
+    return QS_ERR_SHAPE;
+  const int64_t need = qs_block_attention_workspace_bytes(B, Lq, Hq, D, T);
+  if (need < 0 || (flags & ~QS_ATTN_CAUSAL) || !(scale > 0.f) || !std::isfinite(scale))
+    return QS_ERR_RANGE;
+  if (need > 0) {
+    if (!workspace) return QS_ERR_NULL;
+    if (workspace_bytes < need) return QS_ERR_RANGE;
+    if (!aligned16(workspace)) return QS_ERR_ALIGN;
+    QS_TRY(check_device_ptr(workspace));
+  }
+  const qs::attn::Plan p = qs::attn::plan(B, Hq, Lq, T);
+  const int64_t nq = (Lq + QS_BLOCK_Q - 1) / QS_BLOCK_Q;
+  if (nq * p.splits > INT32_MAX || B * Hq * Lq / 8 > INT32_MAX - 1) return QS_ERR_RANGE;
+  QS_TRY(check_ints(blocks));
+  QS_TRY(check_ints(q_len));
+  QS_TRY(check_ints(k_len));
+  if (lse) {
+    if (!aligned_to(lse, 4)) return QS_ERR_ALIGN;
+    QS_TRY(check_device_ptr(lse));
+  }
+  CUtensorMap mq, mk, mv;
+  if (!qs::attn::make_map(&mq, q, D, Lq, Hq, B, q_strides->row, q_strides->head, q_strides->batch,
+                          QS_BLOCK_Q) ||
+      !qs::attn::make_map(&mk, k, D, Lk, Hkv, B, k_strides->row, k_strides->head,
+                          k_strides->batch, QS_BLOCK_K) ||
+      !qs::attn::make_map(&mv, v, D, Lk, Hkv, B, v_strides->row, v_strides->head,
+                          v_strides->batch, QS_BLOCK_K))
+    return QS_ERR_CUDA;
+  qs::attn::Args a{};
+  a.out = out, a.o_batch = out_strides->batch, a.o_row = out_strides->row;
+  a.o_head = out_strides->head, a.lse = lse, a.blocks = blocks;
+  a.q_len = q_len, a.k_len = k_len, a.part = static_cast<float*>(workspace);
+  a.Lq = Lq, a.Lk = Lk, a.B = static_cast<int>(B), a.Hq = static_cast<int>(Hq);
+  a.Hkv = static_cast<int>(Hkv), a.nq = static_cast<int>(nq), a.T = static_cast<int>(T);
+  a.splits = p.splits, a.chunk = p.chunk, a.causal = (flags & QS_ATTN_CAUSAL) != 0;
+  a.scale = scale;
+  a.q_by_head = q_strides->head != 0, a.q_by_batch = q_strides->batch != 0;
+  a.k_by_head = k_strides->head != 0, a.k_by_batch = k_strides->batch != 0;
+  a.v_by_head = v_strides->head != 0, a.v_by_batch = v_strides->batch != 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == QS_F16;
+  const cudaError_t e =
+      D == 64 ? (f16 ? qs::attn::launch<64, true>(mq, mk, mv, a, s) : qs::attn::launch<64, false>(mq, mk, mv, a, s))
+              : (f16 ? qs::attn::launch<128, true>(mq, mk, mv, a, s) : qs::attn::launch<128, false>(mq, mk, mv, a, s));
+  return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
+}
+
 qs_status qs_linear_noalloc(const void* x_bf16, int64_t M, int64_t K, float alpha,
                             const void* w_packed, const float* w_scale, const void* bias_bf16,
                             int64_t N, int bits, void* out_bf16, void* stream) {
@@ -913,6 +1166,7 @@ const char* qs_status_str(int status) {
     case QS_ERR_CUDA: return "CUDA call or launch failed";
     case QS_ERR_TIMEOUT: return "a kernel wait exceeded its bound";
     case QS_ERR_PTR: return "pointer is not device memory of the current device";
+    case QS_ERR_DTYPE: return "element type not taken by this operator";
     default: return "unknown status";
   }
 }

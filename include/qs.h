@@ -65,7 +65,8 @@ typedef enum {
                           or (from qs_device_error) a row index out of range */
   QS_ERR_CUDA = 6,     /* a CUDA runtime/driver call or a launch failed */
   QS_ERR_TIMEOUT = 7,  /* a kernel wait exceeded its bound (reported by qs_device_error) */
-  QS_ERR_PTR = 8       /* a pointer is not device memory of the current device */
+  QS_ERR_PTR = 8,      /* a pointer is not device memory of the current device */
+  QS_ERR_DTYPE = 9     /* an element type that the operator does not take */
 } qs_status;
 
 /* Test-only flag: skip the Hadamard rotation (the codes are then taken from the
@@ -534,6 +535,162 @@ QS_API qs_status qs_linear_gbs(const void* x_bf16, int64_t M, int64_t K, float a
  * QS_ERR_CUDA.
  */
 QS_API qs_status qs_gelu_bf16(const void* x_bf16, int64_t n, void* y_bf16, void* stream);
+
+/*
+ * Operators around the quantised projections of a transformer block: between
+ * the qkv projection and the out projection (rotary positions, the choice of
+ * key blocks, attention over them), and low-rank adapters beside any of them.
+ * QuantSparse quantises the linears and sparsifies attention to 15 % density
+ * (its "Resumen técnico" §2.B, §4); the pages give no kernel of either, the
+ * definitions here are this library's.  All are forward (serving) operators.
+ *
+ * They take views: strides are in ELEMENTS, the last dimension is contiguous.
+ */
+typedef enum { QS_BF16 = 0, QS_F16 = 1, QS_F32 = 2 } qs_dtype;
+
+/* Strides of a [batch, row, head, dim] view, in elements. */
+typedef struct {
+  int64_t batch, row, head;
+} qs_strides;
+
+#define QS_BLOCK_Q 128 /* queries that share a list of key blocks */
+#define QS_BLOCK_K 64  /* keys of a block */
+#define QS_MAX_LEN (1LL << 24)          /* largest Lq or Lk accepted */
+#define QS_MAX_SELECT_BLOCKS 24576      /* key blocks qs_block_select ranks (1.5 M keys) */
+
+#define QS_ROPE_INTERLEAVED 1u /* pairs (x[2p], x[2p+1]); else (x[p], x[p + rot_dim/2]) */
+#define QS_ROPE_INVERSE 2u     /* turns by -a */
+/*
+ * qs_rope — rotary positions.  Pair p (p < rot_dim/2) of every head of row r
+ * turns by a = positions[r][pair_axis[p]] * inv_freq[p]:
+ *   (u, v) -> scale * (u cos a - v sin a, u sin a + v cos a).
+ * The angle is formed and reduced in binary64 (positions up to 2^53 in
+ * magnitude; a product beyond 2^52 has no fractional digits left), the
+ * products are binary32, rounded once.  Elements from rot_dim on are copied.
+ *   x, y        [rows, heads, head_dim] views of dtype QS_BF16, QS_F16 or
+ *               QS_F32, aligned to their elements.  y may be x itself with the
+ *               same strides; otherwise the two must not share elements.  With
+ *               16-byte aligned pointers, strides and head dimensions that
+ *               are multiples of 16 bytes (rot_dim, or rot_dim/2 in halves,
+ *               too) accesses are 16 bytes wide, else single elements.
+ *   rot_dim     even, 2 .. head_dim;  head_dim <= 1024
+ *   positions   [rows, axes] int64 (device, contiguous);  axes 1 .. 8
+ *   pair_axis   [rot_dim/2] int32 (device) or NULL (axis 0 for all); a value
+ *               outside [0, axes) is read as 0 and makes qs_device_error
+ *               report QS_ERR_RANGE
+ *   inv_freq    [rot_dim/2] double (device)
+ *   scale       finite; 1 unless the positions are scaled for long contexts
+ */
+QS_API qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride,
+                         int64_t rows, int64_t heads, int64_t head_dim, int64_t rot_dim,
+                         const int64_t* positions, int axes, const int32_t* pair_axis,
+                         const double* inv_freq, double scale, unsigned flags, int dtype,
+                         void* y, int64_t y_row_stride, int64_t y_head_stride, void* stream);
+
+/*
+ * qs_lora_add — low-rank adapters of many requests beside a shared projection
+ * (packed integer weights cannot take a merged update):
+ *   out[m][n] = bf16(y[m][n] + scale[i] * sum_r B_i[n][r] (sum_k A_i[r][k] x[m][k]))
+ * with i = seg_adapter[s] for the rows seg_start[s] <= m < seg_start[s+1] of
+ * request s.  i = -1: no adapter, out = y there.  Rows outside every request
+ * (in front of the first, behind the last) are left as they were.  Sums in
+ * binary32; the inner one enters the outer as two bf16 numbers (2^-17).
+ *   x_bf16       [M, K], K % 128 == 0, K <= QS_MAX_K
+ *   y_bf16       [M, N], N % 16 == 0: the projection's output
+ *   a_bf16       [adapters, R, K];  b_bf16 [adapters, N, R];  R % 8 == 0,
+ *                8 <= R <= 128 (smaller ranks: zero rows of A)
+ *   scale        [adapters] float, or NULL (1)
+ *   seg_start    [requests + 1] int32 (device), ascending, within [0, M];
+ *   seg_adapter  [requests] int32 (device), -1 .. adapters - 1.  A request
+ *                whose rows or adapter are out of range is left out and makes
+ *                qs_device_error report QS_ERR_RANGE.
+ *   workspace    qs_lora_workspace_bytes(M, K, R, requests) bytes of device
+ *                scratch, 16-byte aligned (-1 for rejected arguments)
+ *   out_bf16     [M, N]; may be y_bf16 itself
+ */
+QS_API int64_t qs_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t requests);
+QS_API qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t K,
+                             int64_t N, const void* a_bf16, const void* b_bf16,
+                             const float* scale, int64_t adapters, int64_t R,
+                             const int32_t* seg_start, const int32_t* seg_adapter,
+                             int64_t requests, void* workspace, int64_t workspace_bytes,
+                             void* out_bf16, void* stream);
+
+/*
+ * Sequence lengths (q_len, k_len, len below): [B] int32 on the device, or NULL
+ * (every sequence is full).  Rows and keys at and behind a length are never
+ * used, whatever they hold.  A length outside [0, L] is held to that range and
+ * makes qs_device_error report QS_ERR_RANGE.
+ *
+ * qs_block_means — the mean of every block of QS_BLOCK_K rows, the cheap key
+ * that qs_block_select scores (binary64 sums rounded once to binary32; 0 for a
+ * block without valid rows).
+ *   x            [B, L, H, D] view, QS_BF16 or QS_F16, D 64 or 128, 16-byte
+ *                aligned, strides multiples of 8 elements
+ *   first_block  blocks before this one are left as they were: a cache that
+ *                grew by some tokens recomputes its last blocks only
+ *   means        [B, H, ceil(L / QS_BLOCK_K), D] float
+ */
+QS_API qs_status qs_block_means(const void* x, const qs_strides* x_strides, int64_t B, int64_t L,
+                                int64_t H, int64_t D, int dtype, const int32_t* len,
+                                int64_t first_block, float* means, void* stream);
+
+#define QS_ATTN_CAUSAL 1u /* query i of a sequence sees keys 0 .. i + k_len - q_len */
+/*
+ * qs_block_select — for each block of QS_BLOCK_Q queries the T visible key
+ * blocks of the highest score <mean of its queries, mean of the keys> (query
+ * means rounded to binary32 as the keys' are, products and sums in binary64;
+ * NaN scores rank last), the lowest index among equals.  A key block is
+ * visible if the query block's last row sees one of its keys.  The first
+ * `keep_first` and the last `keep_last` visible blocks rank above all others.
+ *   q       [B, Lq, Hq, D] view as x of qs_block_means
+ *   means   [B, Hkv, ceil(Lk / QS_BLOCK_K), D] float (qs_block_means), 16-byte
+ *           aligned; Hq % Hkv == 0, query head h reads key head h / (Hq / Hkv);
+ *           at most QS_MAX_SELECT_BLOCKS blocks
+ *   blocks  [B, Hq, ceil(Lq / QS_BLOCK_Q), T] int32, written: ascending, -1
+ *           behind the last (all -1 for a query block behind q_len)
+ */
+QS_API qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B,
+                                 int64_t Lq, int64_t Hq, int64_t D, int dtype,
+                                 const float* means, int64_t Lk, int64_t Hkv,
+                                 const int32_t* q_len, const int32_t* k_len, int64_t T,
+                                 int64_t keep_first, int64_t keep_last, unsigned flags,
+                                 int32_t* blocks, void* stream);
+
+/*
+ * qs_block_attention — softmax(scale q k^T) v over the keys of the listed
+ * blocks that each row sees.  A row that sees none gets 0 (lse -inf).
+ * Tensor-core products of the operands' type with binary32 accumulation,
+ * softmax statistics in binary32; the probabilities enter the second product
+ * rounded to the operands' type.
+ *   q, k, v   [B, Lq, Hq, D], [B, Lk, Hkv, D] x 2 views, QS_BF16 or QS_F16, D 64
+ *             or 128, 16-byte aligned, strides multiples of 8 elements below
+ *             2^39 (a batch or head stride of 0 shares one tensor).  A
+ *             non-finite value in a valid row of v reaches every row of the
+ *             query blocks that list its block, causal or not.
+ *   blocks    [B, Hq, ceil(Lq / QS_BLOCK_Q), T] int32 in any order; -1 is no
+ *             block, a block listed twice counts twice, and a value outside
+ *             [-1, ceil(Lk / QS_BLOCK_K)) is left out and makes
+ *             qs_device_error report QS_ERR_RANGE
+ *   scale     finite, > 0
+ *   workspace qs_block_attention_workspace_bytes(B, Lq, Hq, D, T) bytes of
+ *             device scratch, 16-byte aligned (0: none is needed and it may be
+ *             NULL; -1 for rejected arguments)
+ *   out       [B, Lq, Hq, D] view like q; must not overlap the inputs
+ *   lse       [B, Hq, Lq] float, the log of each row's softmax denominator,
+ *             or NULL
+ * Rows of out and lse at and behind q_len are left as they were.
+ */
+QS_API int64_t qs_block_attention_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t D,
+                                                  int64_t T);
+QS_API qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const void* k,
+                                    const qs_strides* k_strides, const void* v,
+                                    const qs_strides* v_strides, int64_t B, int64_t Lq,
+                                    int64_t Lk, int64_t Hq, int64_t Hkv, int64_t D, int dtype,
+                                    const int32_t* blocks, int64_t T, const int32_t* q_len,
+                                    const int32_t* k_len, float scale, unsigned flags,
+                                    void* workspace, int64_t workspace_bytes, void* out,
+                                    const qs_strides* out_strides, float* lse, void* stream);
 
 /*
  * qs_linear_noalloc — qs_linear for callers that cannot allocate device memory
