@@ -163,6 +163,31 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Two binary32 numbers in one 64-bit register pair: one instruction for two operations.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if (F16) {
@@ -182,6 +207,27 @@ __device__ __forceinline__ int checked_len(const int32_t* len, int b, int64_t mo
     return n < 0 ? 0 : static_cast<int>(most);
   }
   return n;
+}
+
+// A row's 128 scores.
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[4][32]) {
+  uint32_t r[4][32];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(taddr + 32 * q, r[q]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[q][e] = __uint_as_float(r[q][e]);
+}
+
+// -inf for the keys of the two entries from the first that the row does not see.
+__device__ __forceinline__ void mask_scores(float (&s)[4][32], int seen0, int seen1) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (32 * (q & 1) + e >= (q < 2 ? seen0 : seen1)) s[q][e] = -INFINITY;
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -331,20 +377,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       ok = mbar_wait_bounded(bar(kSFull), ph, abort_flag, kErrWaitEpilogue);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      // the row's maximum
-      float top = -INFINITY;
+      float s[4][32];
+      load_scores(tS + mine, s);
+      const int seen0 = limit - j0, seen1 = limit - j1;  // of each entry's keys
+      if (masked) mask_scores(s, seen0, seen1);
+      float top4[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t s[32];
-        tmem_ld_32x32b_x32(tS + mine + 32 * q, s);
-        tmem_wait_ld();
-        const int seen_q = masked ? limit - ((q < 2 ? j0 : j1) + 32 * (q & 1)) : 32;
+        top4[q] = fmaxf(s[q][0], s[q][1]);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = __uint_as_float(s[e]);
-          top = fmaxf(top, e < seen_q ? v : -INFINITY);
-        }
+        for (int e = 2; e < 32; e += 2) top4[q] = max3(top4[q], s[q][e], s[q][e + 1]);
       }
+      const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
       // moves the running maximum (and O and l with it) only when the row outgrows it
       const bool move = top > m && (m == -INFINITY || (top - m) * scale2 > kLazy);
       if (__any_sync(0xffffffffu, move)) {
@@ -361,26 +405,31 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tmem_st_32(tO + mine + 32 * q, o);
           }
+          // the scores are read again rather than held meanwhile
+          load_scores(tS + mine, s);
+          if (masked) mask_scores(s, seen0, seen1);
         }
         m = to;
       }
-      const float shift = m == -INFINITY ? 0.f : m * scale2;
+      const float shift = m == -INFINITY ? 0.f : -m * scale2;
+      const uint64_t scale22 = pair(scale2, scale2), shift2 = pair(shift, shift);
+      uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t s[32], p[16];
-        tmem_ld_32x32b_x32(tS + mine + 32 * q, s);
-        tmem_wait_ld();
-        const int seen_q = masked ? limit - ((q < 2 ? j0 : j1) + 32 * (q & 1)) : 32;
+        uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float x = exp2_approx(fmaf(__uint_as_float(s[2 * e]), scale2, -shift));
-          const float y = exp2_approx(fmaf(__uint_as_float(s[2 * e + 1]), scale2, -shift));
-          const float u = 2 * e < seen_q ? x : 0.f, v = 2 * e + 1 < seen_q ? y : 0.f;
-          l += u + v;
+          float u, v;
+          unpair(fma2(pair(s[q][2 * e], s[q][2 * e + 1]), scale22, shift2), u, v);
+          u = exp2_approx(u), v = exp2_approx(v);
+          sum[e & 1] = add2(sum[e & 1], pair(u, v));
           p[e] = pack2<F16>(u, v);
         }
         tmem_st_16(tS + mine + 16 * q, p);
       }
+      float l0, l1;
+      unpair(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
       // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
       if (masked && (j0 + kBK > kl || (j1 < kl && j1 + kBK > kl))) {
         ok = mbar_wait_bounded(bar(kVFull), ph, abort_flag, kErrWaitTma);
