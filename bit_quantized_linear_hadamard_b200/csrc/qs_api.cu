@@ -1087,7 +1087,7 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
   }
   const qs::attn::Plan p = qs::attn::plan(B, Hq, Lq, T);
   const int64_t nq = (Lq + QS_BLOCK_Q - 1) / QS_BLOCK_Q;
-  if (nq * p.splits > INT32_MAX || B * Hq * Lq / 8 > INT32_MAX - 1) return QS_ERR_RANGE;
+  if (B * Hq * nq * p.splits > INT32_MAX || B * Hq * Lq / 8 > INT32_MAX - 1) return QS_ERR_RANGE;
   QS_TRY(check_ints(blocks));
   QS_TRY(check_ints(q_len));
   QS_TRY(check_ints(k_len));
@@ -1095,6 +1095,8 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
     if (!aligned_to(lse, 4)) return QS_ERR_ALIGN;
     QS_TRY(check_device_ptr(lse));
   }
+  const int sms = qs::sm_count();
+  if (sms <= 0) return QS_ERR_CUDA;
   CUtensorMap mq, mk, mv;
   if (!qs::attn::make_map(&mq, q, D, Lq, Hq, B, q_strides->row, q_strides->head, q_strides->batch,
                           QS_BLOCK_Q) ||
@@ -1117,8 +1119,8 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = dtype == QS_F16;
   const cudaError_t e =
-      D == 64 ? (f16 ? qs::attn::launch<64, true>(mq, mk, mv, a, s) : qs::attn::launch<64, false>(mq, mk, mv, a, s))
-              : (f16 ? qs::attn::launch<128, true>(mq, mk, mv, a, s) : qs::attn::launch<128, false>(mq, mk, mv, a, s));
+      D == 64 ? (f16 ? qs::attn::launch<64, true>(mq, mk, mv, a, sms, s) : qs::attn::launch<64, false>(mq, mk, mv, a, sms, s))
+              : (f16 ? qs::attn::launch<128, true>(mq, mk, mv, a, sms, s) : qs::attn::launch<128, false>(mq, mk, mv, a, sms, s));
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 

@@ -5,24 +5,28 @@
 // behind the row's own place).  A row that sees none gets 0 and -inf.
 //
 // Bound by the tensor cores and the exponentials together: a pair of a query row and a key costs
-// 4 D multiply-adds' worth of tensor work and one exponential, and at D = 128 both take about the
-// same time on an SM.  One CTA holds one query block; two CTAs share an SM, so that one's
-// products run while the other takes exponentials.
+// 4 D operations on the tensor cores and one exponential, and at D = 128 both take about the same
+// time on an SM.  So the row threads must never wait for a product, nor the products for them.
 //
-// A CTA's tile is two list entries, 128 keys.  Warps 0-3 own one query row per thread (lane of
-// the tensor memory): the row's maximum and sum need no exchange between threads.  Warp 4 loads
-// K and V by TMA (one 128-key tile of each in shared memory; K of the next tile is fetched as
-// soon as this tile's scores are formed, V as soon as its product is), warp 5 issues the MMAs:
-//   S = Q K^T into tensor memory (binary32), P (bf16 or fp16) written over S by the row threads,
-//   O += P V with P read from tensor memory and V as the MN-major operand.
-// O stays in tensor memory.  The running maximum only moves when a row's scores exceed it by
-// 2^8: until then the old one serves (P stays below 2^8, in range of both types), and most tiles
-// need no pass over O.  P is rounded to the operands' type (the tensor cores take no other);
-// the row's sum is of the unrounded values in binary32.
+// One persistent CTA per SM works through the (batch, head, query block, split) items.  A tile is
+// two of an item's listed blocks, 128 keys: an MMA of 64 columns takes as long as one of 128
+// (measured 70 and 75 cycles at K = 16), so blocks go in pairs.  Three groups of 128 threads own
+// one query row per thread (lane of the tensor memory) and take the tiles in turn, each with a
+// score buffer of its own; O fills the rest of the tensor memory:
+//   S = Q K^T (binary32), P (bf16 or fp16) written over S by the row threads, O += P V.
+// While one group takes its exponentials, the products of the other two run, and a group has the
+// time of two tiles to get through its part.
 //
-// Long lists with few query blocks (a single token) are cut into `splits` ranges that run on CTAs
-// of their own and leave normalised binary32 parts with their lse; a second kernel joins them in
-// order.
+// A row's running maximum goes from group to group in the order of the tiles, before the
+// exponentials.  It only moves when the scores exceed it by 2^8: until then the old one serves (P
+// stays below 2^8, in range of both types), and O, which all groups share, is hardly ever
+// rescaled.  P is rounded to the operands' type (the tensor cores take no other); a row's sums,
+// one per group, are of the unrounded values in binary32.
+// Warps 0-11 the three groups; 12 and 14 read the lists and load Q and K, and V, by TMA; 13 and
+// 15 issue the MMAs of S and of O.
+//
+// With few items (a single token) the lists are cut into `splits` ranges that are items of their
+// own and leave normalised binary32 parts with their lse; a second kernel joins them in order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,27 +42,45 @@ namespace qs {
 namespace attn {
 
 constexpr int kBQ = QS_BLOCK_Q, kBK = QS_BLOCK_K, kTileK = 2 * kBK;
-constexpr int kRowWarps = 4;
-constexpr int kThreads = 32 * (kRowWarps + 2);
-constexpr int kMaxList = 2048;  // list entries of one CTA
-constexpr int kTmemCols = 256;  // S (128) and O (up to 128)
+constexpr int kGroups = 3, kGroupWarps = 4;
+constexpr int kTmaWarp = kGroups * kGroupWarps, kMmaWarp = kTmaWarp + 1, kTmaVWarp = kMmaWarp + 1,
+              kPvWarp = kTmaVWarp + 1;
+constexpr int kThreads = 32 * 16;  // 128 registers each
 constexpr int kSms = 148;
-constexpr float kLazy = 8.f;    // log2 of the factor a row may exceed its running maximum by
+constexpr float kLazy = 8.f;  // log2 of the factor a row may exceed its running maximum by
+constexpr int kTileRing = 8, kItemRing = 4;
 
-enum { kQFull, kKFull, kKEmpty, kVFull, kVEmpty, kSFull, kPFull, kOFull, kDrain, kNumBars };
+// Tensor memory, columns of 32 bits: O, then the groups' score buffers.
+constexpr int kTmemCols = 512, kColO = 0, kColS = 128;
 
 template <int D>
 struct Cfg {
-  static constexpr int kHalves = D / 64;               // 128-byte wide operand columns
-  static constexpr int kHalf = 128 * 128;              // bytes of 128 rows of one of them
+  static constexpr int kHalves = D / 64;         // 128-byte wide operand columns
+  static constexpr int kHalf = kTileK * 128;     // bytes of 128 rows in one of them
   static constexpr int kOp = kHalves * kHalf;
-  static constexpr int kOffQ = 0, kOffK = kOp, kOffV = 2 * kOp, kOffList = 3 * kOp;
-  static constexpr int kOffBar = kOffList + 4 * kMaxList;
+  static constexpr int kStages = 256 / D;        // of the K and V rings: 64 KB each
+  static constexpr int kOffQ = 0, kOffK = 2 * kOp, kOffV = kOffK + kStages * kOp;
+  static constexpr int kOffM = kOffV + kStages * kOp;              // running maxima, per group
+  static constexpr int kOffMl = kOffM + kGroups * kBQ * 4;         // (m, l) per group, two items
+  static constexpr int kOffTiles = kOffMl + 2 * kGroups * kBQ * 8; // first keys of a tile's blocks
+  static constexpr int kOffItems = kOffTiles + 8 * kTileRing;      // (item, tiles)
+  static constexpr int kOffBar = kOffItems + 8 * kItemRing;
+  // barriers
+  static constexpr int kKFull = 0, kKEmpty = kStages, kVFull = 2 * kStages, kVEmpty = 3 * kStages;
+  static constexpr int kQFull = 4 * kStages, kQFree = kQFull + 2, kSFull = kQFree + 2;
+  static constexpr int kPFull = kSFull + kGroups, kPvDone = kPFull + kGroups;
+  static constexpr int kMReady = kPvDone + kGroups;  // per group and warp
+  static constexpr int kOFree = kMReady + kGroups * kGroupWarps, kTileFull = kOFree + 1;
+  static constexpr int kItemFull = kTileFull + kTileRing, kItemEmpty = kItemFull + kItemRing;
+  static constexpr int kDrain = kItemEmpty + kItemRing, kNumBars = kDrain + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  // two CTAs per SM and no more (each holds half of the tensor memory), whatever D
-  static constexpr int kNeed = kOffMisc + 32 + 1024;
-  static constexpr int kSmemBytes = kNeed > 100 * 1024 ? kNeed : 100 * 1024;
-  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  __device__ static int arrivals(int i) {
+    if ((i >= kPFull && i < kPvDone) || i == kOFree) return i == kOFree ? kGroups * kGroupWarps : kGroupWarps;
+    if (i >= kItemEmpty && i < kDrain) return kGroups * kGroupWarps + 2;
+    return 1;
+  }
 };
 
 struct Args {
@@ -129,6 +151,30 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Whether the phase has completed, without the suspension of try_wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -136,20 +182,6 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[1
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -209,31 +241,86 @@ __device__ __forceinline__ int checked_len(const int32_t* len, int b, int64_t mo
   return n;
 }
 
-// A row's 128 scores.
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[4][32]) {
-  uint32_t r[4][32];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(taddr + 32 * q, r[q]);
+// 64 scores of a row: those of one block.
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[64]) {
+  uint32_t r[2][32];
+  tmem_ld_32x32b_x32(taddr, r[0]);
+  tmem_ld_32x32b_x32(taddr + 32, r[1]);
   tmem_wait_ld();
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int e = 0; e < 32; ++e) s[q][e] = __uint_as_float(r[q][e]);
+  for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(r[e / 32][e % 32]);
 }
 
-// -inf for the keys of the two entries from the first that the row does not see.
-__device__ __forceinline__ void mask_scores(float (&s)[4][32], int seen0, int seen1) {
+// -inf for the keys that the row does not see.
+__device__ __forceinline__ void mask_scores(float (&s)[64], int seen) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int e = 0; e < 64; ++e)
+    if (e >= seen) s[e] = -INFINITY;
+}
+
+__device__ __forceinline__ float max64(const float (&s)[64]) {
+  float top[4];
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (32 * (q & 1) + e >= (q < 2 ? seen0 : seen1)) s[q][e] = -INFINITY;
+  for (int q = 0; q < 4; ++q) {
+    top[q] = fmaxf(s[16 * q], s[16 * q + 1]);
+#pragma unroll
+    for (int e = 2; e < 16; e += 2) top[q] = max3(top[q], s[16 * q + e], s[16 * q + e + 1]);
+  }
+  return fmaxf(max3(top[0], top[1], top[2]), top[3]);
+}
+
+// P = exp2(scale2 * s + shift) of 64 scores into tensor memory; their sum is added to `sum`.
+template <bool F16>
+__device__ __forceinline__ void exp_scores(uint32_t taddr, const float (&s)[64], uint64_t scale2,
+                                           uint64_t shift2, uint64_t (&sum)[2]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float u, v;
+      unpair(fma2(pair(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), scale2, shift2), u, v);
+      u = exp2_approx(u), v = exp2_approx(v);
+      sum[e & 1] = add2(sum[e & 1], pair(u, v));
+      p[e] = pack2<F16>(u, v);
+    }
+    tmem_st_16(taddr + 16 * q, p);
+  }
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// One item: a range of the list of one query block.
+struct Item {
+  int b, h, hk, qb, split;
+  int ql, kl, row0, rows, off, seen;
+  const int32_t* list;
+  int len;  // entries of the range; 0 behind the sequence
+};
+
+__device__ __forceinline__ Item item_at(const Args& a, unsigned i) {
+  Item it;
+  it.split = static_cast<int>(i % static_cast<unsigned>(a.splits));
+  i /= static_cast<unsigned>(a.splits);
+  it.qb = static_cast<int>(i % static_cast<unsigned>(a.nq));
+  i /= static_cast<unsigned>(a.nq);
+  it.h = static_cast<int>(i % static_cast<unsigned>(a.Hq));
+  it.b = static_cast<int>(i / static_cast<unsigned>(a.Hq));
+  it.hk = it.h / (a.Hq / a.Hkv);
+  it.ql = checked_len(a.q_len, it.b, a.Lq);
+  it.kl = checked_len(a.k_len, it.b, a.Lk);
+  it.row0 = it.qb * kBQ;
+  it.rows = min(kBQ, it.ql - it.row0);  // <= 0 behind the sequence: such rows stay as they are
+  it.off = it.kl - it.ql;               // causal: row i sees keys up to i + off
+  it.seen = a.causal ? min(it.kl, it.row0 + it.rows + it.off) : it.kl;  // by the last row
+  it.list = a.blocks + ((static_cast<int64_t>(it.b) * a.Hq + it.h) * a.nq + it.qb) * a.T +
+            static_cast<int64_t>(it.split) * a.chunk;
+  it.len = it.rows > 0 ? min(a.chunk, a.T - it.split * a.chunk) : 0;
+  return it;
+}
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const Args a) {
   using C = Cfg<D>;
@@ -242,257 +329,378 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
   uint8_t* sp = smem_raw + pad;
   const uint32_t sbase = raw + pad;
-  int* list = reinterpret_cast<int*>(sp + C::kOffList);
+  float* maxima = reinterpret_cast<float*>(sp + C::kOffM);  // [group][row]
+  float2* ml = reinterpret_cast<float2*>(sp + C::kOffMl);   // [item parity][group][row]
+  int2* tile_ring = reinterpret_cast<int2*>(sp + C::kOffTiles);
+  int2* item_ring = reinterpret_cast<int2*>(sp + C::kOffItems);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + C::kOffMisc + 4);
-  int* list_len = reinterpret_cast<int*>(sp + C::kOffMisc + 8);
   const auto bar = [&](int i) { return sbase + C::kOffBar + 8u * i; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qb = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hkv);
-  const int ql = checked_len(a.q_len, b, a.Lq), kl = checked_len(a.k_len, b, a.Lk);
-  const int row0 = qb * kBQ;
-  if (row0 >= ql) return;  // rows behind the sequence stay as they are
-  const int off = kl - ql;  // causal: row i sees keys up to i + off
-  const int rows = min(kBQ, ql - row0);
-  const int seen = a.causal ? min(kl, row0 + rows + off) : kl;  // keys the last row sees
+  const unsigned items = static_cast<unsigned>(a.B) * a.Hq * a.nq * a.splits;  // below 2^31
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), i == kPFull ? 32 * kRowWarps : 1);
+    for (int i = 0; i < C::kNumBars; ++i) mbar_init(bar(i), C::arrivals(i));
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 4) {  // the list's entries that some row of the block sees
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
-    const int32_t* src = a.blocks + ((static_cast<int64_t>(b) * a.Hq + h) * a.nq + qb) * a.T;
-    const int end = min(a.T, (split + 1) * a.chunk);
-    const int64_t nk = (a.Lk + kBK - 1) / kBK;
-    int n = 0;
-    for (int i0 = split * a.chunk; i0 < end; i0 += 32) {
-      const int j = i0 + lane < end ? src[i0 + lane] : -1;
-      if (j < -1 || j >= nk) atomicOr(&g_error_word, kErrIndex);
-      const bool take = j >= 0 && j < nk && j * kBK < seen;
-      const unsigned got = __ballot_sync(0xffffffffu, take);
-      if (take) list[n + __popc(got & ((1u << lane) - 1u))] = j;
-      n += __popc(got);
-    }
-    if (lane == 0) *list_len = n;
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n = *list_len, tiles = (n + 1) / 2;
-  const uint32_t tS = tmem, tO = tmem + 128;
 
-  if (warp == 4) {
-    if (lane == 0 && tiles > 0) {
-      mbar_arrive_expect_tx(bar(kQFull), C::kOp);
-      for (int d = 0; d < C::kHalves; ++d)
-        tma_load_4d(sbase + C::kOffQ + d * C::kHalf, &tmQ, 64 * d, row0, h * a.q_by_head,
-                    b * a.q_by_batch, bar(kQFull));
-      const int kh = hk * a.k_by_head, kb = b * a.k_by_batch;
-      const int vh = hk * a.v_by_head, vb = b * a.v_by_batch;
-      int k_loads = 0, v_loads = 0;
-      for (int t = 0; t < tiles; ++t) {
-        // a missing second entry is loaded from behind the last key: zeros
-        const int r0 = list[2 * t] * kBK;
-        const int r1 = 2 * t + 1 < n ? list[2 * t + 1] * kBK : static_cast<int>(a.Lk);
-        if (!mbar_wait_bounded(bar(kKEmpty), (t & 1) ^ 1u, abort_flag, kErrWaitProducer)) break;
-        mbar_arrive_expect_tx(bar(kKFull), C::kOp);
-        for (int d = 0; d < C::kHalves; ++d) {
-          const uint32_t dst = sbase + C::kOffK + d * C::kHalf;
-          tma_load_4d(dst, &tmK, 64 * d, r0, kh, kb, bar(kKFull));
-          tma_load_4d(dst + C::kHalf / 2, &tmK, 64 * d, r1, kh, kb, bar(kKFull));
+  // After a wait that gave up, every role runs through to its end without waiting or issuing
+  // anything more, so that all threads still meet at the barriers.
+  bool ok = true;
+  const auto wait = [&](int i, uint32_t parity, unsigned err) {
+    if (ok) ok = mbar_wait_bounded(bar(i), parity, abort_flag, err);
+  };
+
+  if (warp < kTmaWarp) {
+    // ---- row groups.  A barrier of parity p is only ever waited on when its phase before the
+    // awaited one is known to be complete: S of tile g is formed when P V of tile g - 3 is done.
+    const int group = warp / kGroupWarps, quarter = warp % kGroupWarps;
+    const int r = threadIdx.x % kBQ;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t tS = tmem + kColS + kTileK * group + lanes, tO = tmem + kColO + lanes;
+    const float scale2 = a.scale * kLog2e;
+    const uint64_t scale22 = pair(scale2, scale2);
+    unsigned g0 = 0;    // tiles of the items so far
+    for (unsigned e = 0;; ++e) {
+      const int item_slot = e % kItemRing;
+      wait(C::kItemFull + item_slot, (e / kItemRing) & 1, kErrWaitProducer);
+      __syncwarp();
+      const int2 entry = item_ring[item_slot];
+      // an aborted block leaves together: the flag was up before any thread's wait gave up, but
+      // threads may differ on this wait, so all agree at the barrier below
+      const int leave = entry.x < 0 || !ok;
+      int any_leave;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+          "barrier.cta.red.or.pred q, 2, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+          : "=r"(any_leave)
+          : "r"(leave), "n"(32 * kTmaWarp)
+          : "memory");
+      if (any_leave) break;
+      if (lane == 0) mbar_arrive(bar(C::kItemEmpty + item_slot));
+      const Item it = item_at(a, static_cast<unsigned>(entry.x));
+      const int n = entry.y;
+      const int row = it.row0 + r;
+      const int limit = a.causal ? min(it.kl, row + it.off + 1) : it.kl;    // keys this row sees
+      const int full = a.causal ? min(it.kl, it.row0 + it.off + 1) : it.kl; // keys every row sees
+      float m = -INFINITY, l = 0.f;
+      // tiles of this group: those with (g0 + t) % 3 == group
+      for (int t = (group + kGroups - static_cast<int>(g0 % kGroups)) % kGroups; t < n; t += kGroups) {
+        const unsigned g = g0 + t;
+        const uint32_t ph = (g / kGroups) & 1;
+        wait(C::kTileFull + g % kTileRing, (g / kTileRing) & 1, kErrWaitProducer);
+        wait(C::kSFull + group, ph, kErrWaitEpilogue);
+        __syncwarp();
+        tc_fence_after();
+        const int2 tile = tile_ring[g % kTileRing];
+        const bool masked = tile.x + kBK > full || tile.y + kBK > full;
+        float s[64];
+        load_scores(tS + kBK, s);
+        if (masked) mask_scores(s, limit - tile.y);
+        float top = max64(s);
+        load_scores(tS, s);
+        if (masked) mask_scores(s, limit - tile.x);
+        top = fmaxf(top, max64(s));
+        // the running maximum from the tile before; it moves only when the row outgrows it
+        float old = -INFINITY;
+        if (t > 0) {
+          const int from = (group + kGroups - 1) % kGroups;
+          wait(C::kMReady + from * kGroupWarps + quarter, ((g - 1) / kGroups) & 1, kErrWaitEpilogue);
+          __syncwarp();
+          old = maxima[from * kBQ + r];
         }
-        ++k_loads;
-        if (!mbar_wait_bounded(bar(kVEmpty), (t & 1) ^ 1u, abort_flag, kErrWaitProducer)) break;
-        mbar_arrive_expect_tx(bar(kVFull), C::kOp);
-        for (int d = 0; d < C::kHalves; ++d) {
-          const uint32_t dst = sbase + C::kOffV + d * C::kHalf;
-          tma_load_4d(dst, &tmV, 64 * d, r0, vh, vb, bar(kVFull));
-          tma_load_4d(dst + C::kHalf / 2, &tmV, 64 * d, r1, vh, vb, bar(kVFull));
-        }
-        ++v_loads;
-      }
-      // no copy into this CTA's memory may outlive it
-      mbar_wait_limit(bar(kQFull), 0, kWaitTimeoutNs, kErrWaitTma);
-      if (k_loads) mbar_wait_limit(bar(kKFull), (k_loads - 1) & 1, kWaitTimeoutNs, kErrWaitTma);
-      if (v_loads) mbar_wait_limit(bar(kVFull), (v_loads - 1) & 1, kWaitTimeoutNs, kErrWaitTma);
-    }
-  } else if (warp == 5) {
-    if (lane == 0 && tiles > 0) {
-      constexpr uint32_t idesc_s = idesc_f16(128, 128, F16, false);
-      constexpr uint32_t idesc_o = idesc_f16(128, D, F16, true);
-      if (mbar_wait_bounded(bar(kQFull), 0, abort_flag, kErrWaitTma)) {
-        for (int t = 0; t < tiles; ++t) {
-          const uint32_t ph = t & 1;
-          if (!mbar_wait_bounded(bar(kKFull), ph, abort_flag, kErrWaitTma)) break;
+        const bool move = top > old && (old == -INFINITY || (top - old) * scale2 > kLazy);
+        const float now = move ? top : old;
+        maxima[group * kBQ + r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kMReady + group * kGroupWarps + quarter));
+        if (t > 0 && __any_sync(0xffffffffu, move)) {
+          wait(C::kPvDone + (g - 1) % kGroups, ((g - 1) / kGroups) & 1, kErrWaitEpilogue);
+          __syncwarp();
           tc_fence_after();
+          const float f = !move ? 1.f : old == -INFINITY ? 0.f : exp2_approx((old - now) * scale2);
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld_16(tO + 16 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st_16(tO + 16 * q, o);
+          }
+        }
+        if (m != now) {  // this group's sum moves with it
+          l = m == -INFINITY ? 0.f : l * exp2_approx((m - now) * scale2);
+          m = now;
+        }
+        const float shift = m == -INFINITY ? 0.f : -m * scale2;
+        const uint64_t shift2 = pair(shift, shift);
+        uint64_t sum[2] = {0ull, 0ull};
+        exp_scores<F16>(tS, s, scale22, shift2, sum);
+        load_scores(tS + kBK, s);
+        if (masked) mask_scores(s, limit - tile.y);
+        exp_scores<F16>(tS + kBK / 2, s, scale22, shift2, sum);
+        float l0, l1;
+        unpair(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+        // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
+        if (tile.x + kBK > it.kl || (tile.y < it.kl && tile.y + kBK > it.kl)) {
+          const int slot = static_cast<int>(g % C::kStages);
+          wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
+          const int key = r < kBK ? tile.x + r : tile.y + r - kBK;  // this thread's row of V
+          if (ok && key >= it.kl)
+            for (int d = 0; d < C::kHalves; ++d)
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(sp + C::kOffV + slot * C::kOp + d * C::kHalf + r * 128 +
+                                          16 * k) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kPFull + group));
+      }
+      g0 += n;
+      // the item's end: the groups' sums meet, then 32 columns of O at a time go to a group
+      ml[((e & 1) * kGroups + group) * kBQ + r] = make_float2(m, l);
+      asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kTmaWarp) : "memory");
+      if (n > 0) wait(C::kPvDone + (g0 - 1) % kGroups, ((g0 - 1) / kGroups) & 1, kErrWaitEpilogue);
+      __syncwarp();
+      tc_fence_after();
+      float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) mm = fmaxf(mm, ml[((e & 1) * kGroups + k) * kBQ + r].x);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        const float2 v = ml[((e & 1) * kGroups + k) * kBQ + r];
+        if (v.x != -INFINITY) sum += v.y * exp2_approx((v.x - mm) * scale2);
+      }
+      // a sum of 0: no key seen; NaN goes on into the row
+      const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
+      const float lse = sum > 0.f ? (mm * scale2 + log2f(sum)) * kLn2 : (sum == sum ? -INFINITY : sum);
+      const int64_t flat = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Lq + row;
+      const int64_t parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
+      const bool write = r < it.rows && ok;
+      if (write && group == kGroups - 1) {
+        if (a.splits > 1)
+          a.part[parts * D * a.splits + it.split * parts + flat] = lse;
+        else if (a.lse)
+          a.lse[flat] = lse;
+      }
+#pragma unroll 1
+      for (int q = group; q < D / 32; q += kGroups) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + 32 * q, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+        if (write && a.splits > 1) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part + (it.split * parts + flat) * D + 32 * q);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (write) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + it.b * a.o_batch +
+                                                row * a.o_row + it.h * a.o_head + 32 * q);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack2<F16>(__uint_as_float(o[8 * k + 2 * j]),
+                                __uint_as_float(o[8 * k + 2 * j + 1]));
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (n > 0 && lane == 0) mbar_arrive(bar(C::kOFree));
+    }
+  } else if (warp == kTmaWarp || warp == kTmaVWarp) {
+    // ---- the lists, and Q, K and V by TMA: one warp announces the items and loads Q and K, the
+    // other V, as K is wanted up to three tiles before V.  The tiles of an item are pairs of its
+    // entries that some row of the block sees; a warp looks at 32 entries at a time.
+    const bool is_v = warp == kTmaVWarp;
+    const int64_t nk = (a.Lk + kBK - 1) / kBK;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
+    const uint32_t ring = sbase + (is_v ? C::kOffV : C::kOffK);
+    const int bar_full = is_v ? C::kVFull : C::kKFull, bar_empty = is_v ? C::kVEmpty : C::kKEmpty;
+    unsigned g = 0, e = 0, loaded_q = 0, loaded = 0;
+    const auto list_part = [&](const Item& it, int i0, int& entry) {
+      entry = i0 + lane < it.len ? __ldg(it.list + i0 + lane) : -1;
+      const bool bad = entry < -1 || entry >= nk;
+      if (bad) atomicOr(&g_error_word, kErrIndex);
+      return __ballot_sync(0xffffffffu, entry >= 0 && !bad && entry * kBK < it.seen);
+    };
+    const auto agree = [&] { ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0; };
+    const auto announce = [&](int item, int tiles) {
+      const int slot = e % kItemRing;
+      if (lane == 0) {
+        wait(C::kItemEmpty + slot, ((e / kItemRing) & 1) ^ 1, kErrWaitProducer);
+        item_ring[slot] = make_int2(item, tiles);
+        mbar_arrive(bar(C::kItemFull + slot));
+      }
+      ++e;
+      agree();
+    };
+    for (unsigned i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      const Item it = item_at(a, i);
+      if (it.rows <= 0) continue;
+      int entry;
+      if (!is_v) {
+        int n = 0;
+        for (int i0 = 0; i0 < it.len; i0 += 32) n += __popc(list_part(it, i0, entry));
+        const int tiles = (n + 1) / 2;
+        announce(static_cast<int>(i), tiles);
+        if (tiles == 0) continue;
+        if (lane == 0) {
+          const int qb = loaded_q & 1;
+          wait(C::kQFree + qb, ((loaded_q >> 1) & 1) ^ 1, kErrWaitProducer);
+          if (ok) {
+            mbar_arrive_expect_tx(bar(C::kQFull + qb), C::kOp);
+            for (int d = 0; d < C::kHalves; ++d)
+              tma_load_4d(sbase + C::kOffQ + qb * C::kOp + d * C::kHalf, &tmQ, 64 * d, it.row0,
+                          it.h * a.q_by_head, it.b * a.q_by_batch, bar(C::kQFull + qb));
+            ++loaded_q;
+          }
+        }
+        agree();
+      }
+      const int hc = it.hk * (is_v ? a.v_by_head : a.k_by_head);
+      const int bc = it.b * (is_v ? a.v_by_batch : a.k_by_batch);
+      const auto load_tile = [&](int j0, int j1) {  // lane 0
+        const int slot = static_cast<int>(g % C::kStages);
+        wait(bar_empty + slot, ((g / C::kStages) & 1) ^ 1, kErrWaitProducer);
+        if (!ok) return;
+        if (!is_v) {
+          // a missing second block: no key of it is seen, and it is loaded from behind the last
+          // key, as zeros
+          tile_ring[g % kTileRing] = make_int2(j0, j1 < a.Lk ? j1 : 0x40000000);
+          mbar_arrive(bar(C::kTileFull + g % kTileRing));
+        }
+        const uint32_t full = bar(bar_full + slot), dst = ring + slot * C::kOp;
+        mbar_arrive_expect_tx(full, C::kOp);
+        for (int d = 0; d < C::kHalves; ++d) {
+          tma_load_4d(dst + d * C::kHalf, map, 64 * d, j0, hc, bc, full);
+          tma_load_4d(dst + d * C::kHalf + C::kHalf / 2, map, 64 * d, j1, hc, bc, full);
+        }
+        ++loaded;
+      };
+      int first = -1;  // a tile's first block, waiting for its second
+      for (int i0 = 0; i0 < it.len && ok; i0 += 32) {
+        for (unsigned bits = list_part(it, i0, entry); bits; bits &= bits - 1) {
+          const int j = __shfl_sync(0xffffffffu, entry, __ffs(bits) - 1) * kBK;
+          if (first < 0) {
+            first = j;
+            continue;
+          }
+          if (lane == 0) load_tile(first, j);
+          first = -1;
+          ++g;
+        }
+        agree();
+      }
+      if (first >= 0) {
+        if (lane == 0) load_tile(first, static_cast<int>(a.Lk));
+        ++g;
+        agree();
+      }
+    }
+    if (!is_v) announce(-1, 0);
+    // no copy into this CTA's memory may outlive it
+    if (lane == 0) {
+      for (unsigned k = loaded_q > 2 ? loaded_q - 2 : 0; k < loaded_q; ++k)
+        mbar_wait_limit(bar(C::kQFull + (k & 1)), (k >> 1) & 1, kWaitTimeoutNs, kErrWaitTma);
+      for (unsigned k = loaded > C::kStages ? loaded - C::kStages : 0; k < loaded; ++k)
+        mbar_wait_limit(bar(bar_full + k % C::kStages), (k / C::kStages) & 1, kWaitTimeoutNs,
+                        kErrWaitTma);
+    }
+  } else if (lane == 0) {
+    // ---- MMAs: one thread issues the scores, another the second products.  An issuing thread
+    // stands still while the tensor cores catch up, and what it has to look at between two tiles
+    // would leave them idle; two threads cover for each other.
+    const bool is_pv = warp == kPvWarp;
+    unsigned g = 0, q = 0;  // tiles, items with tiles
+    for (unsigned e = 0; ok; ++e) {
+      const int item_slot = e % kItemRing;
+      wait(C::kItemFull + item_slot, (e / kItemRing) & 1, kErrWaitMma);
+      if (!ok) break;
+      const int2 entry = item_ring[item_slot];
+      mbar_arrive(bar(C::kItemEmpty + item_slot));
+      if (entry.x < 0) break;
+      if (entry.y == 0) continue;
+      const int qb = q & 1;
+      if (!is_pv) {
+        constexpr uint32_t idesc = idesc_f16(128, kTileK, F16, false);
+        wait(C::kQFull + qb, (q >> 1) & 1, kErrWaitTma);
+        const uint32_t aq = sbase + C::kOffQ + qb * C::kOp;
+        for (int t = 0; t < entry.y && ok; ++t, ++g) {
+          const int slot = static_cast<int>(g % C::kStages), buf = static_cast<int>(g % kGroups);
+          // the buffer is free when P V of the tile three before is done
+          wait(C::kPvDone + buf, ((g / kGroups) & 1) ^ 1, kErrWaitMma);
+          wait(C::kKFull + slot, (g / C::kStages) & 1, kErrWaitTma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t bk = sbase + C::kOffK + slot * C::kOp;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t at = (s / 4) * C::kHalf + (s % 4) * 32;
-            mma_ss(tS, smem_desc_sw128(sbase + C::kOffQ + at),
-                   smem_desc_sw128(sbase + C::kOffK + at), idesc_s, s != 0);
+            mma_ss(tmem + kColS + kTileK * buf, smem_desc_sw128(aq + at), smem_desc_sw128(bk + at),
+                   idesc, s != 0);
           }
-          mma_commit(bar(kSFull));
-          mma_commit(bar(kKEmpty));
-          if (!mbar_wait_bounded(bar(kVFull), ph, abort_flag, kErrWaitTma)) break;
-          if (!mbar_wait_bounded(bar(kPFull), ph, abort_flag, kErrWaitMma)) break;
+          mma_commit(bar(C::kSFull + buf));
+          mma_commit(bar(C::kKEmpty + slot));
+        }
+        mma_commit(bar(C::kQFree + qb));
+      } else {
+        constexpr uint32_t idesc = idesc_f16(128, D, F16, true);
+        // O is free when the item before has been written out
+        wait(C::kOFree, (q & 1) ^ 1, kErrWaitEpilogue);
+        for (int t = 0; t < entry.y && ok; ++t, ++g) {
+          const int slot = static_cast<int>(g % C::kStages), buf = static_cast<int>(g % kGroups);
+          wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
+          wait(C::kPFull + buf, (g / kGroups) & 1, kErrWaitMma);
+          if (!ok) break;
           tc_fence_after();
+          const uint32_t bv = sbase + C::kOffV + slot * C::kOp;
 #pragma unroll
           for (int s = 0; s < kTileK / 16; ++s)
-            mma_ts(tO, tS + 8 * s, smem_desc_mn(sbase + C::kOffV + s * 2048, C::kHalf), idesc_o,
-                   t != 0 || s != 0);
-          mma_commit(bar(kVEmpty));
-          if (t + 1 == tiles) mma_commit(bar(kOFull));
+            mma_ts(tmem + kColO, tmem + kColS + kTileK * buf + 8 * s,
+                   smem_desc_mn(bv + s * 2048, C::kHalf), idesc, t != 0 || s != 0);
+          mma_commit(bar(C::kPvDone + buf));
+          mma_commit(bar(C::kVEmpty + slot));
         }
       }
-      // the tensor memory is given back only when nothing writes it any more
-      mma_commit(bar(kDrain));
-      mbar_wait_limit(bar(kDrain), 0, kWaitTimeoutNs, kErrWaitMma);
+      ++q;
     }
-  } else {
-    const int r = 32 * warp + lane, row = row0 + r;
-    const uint32_t mine = static_cast<uint32_t>(32 * warp) << 16;  // the warp's lanes
-    const int limit = a.causal ? min(kl, row + off + 1) : kl;      // keys this row sees
-    const int full = a.causal ? min(kl, row0 + off + 1) : kl;      // keys every row sees
-    const float scale2 = a.scale * kLog2e;
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int t = 0; t < tiles; ++t) {
-      const uint32_t ph = t & 1;
-      const int j0 = list[2 * t] * kBK;
-      const int j1 = 2 * t + 1 < n ? list[2 * t + 1] * kBK : 0x40000000;
-      const bool masked = j0 + kBK > full || j1 + kBK > full;
-      ok = mbar_wait_bounded(bar(kSFull), ph, abort_flag, kErrWaitEpilogue);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      float s[4][32];
-      load_scores(tS + mine, s);
-      const int seen0 = limit - j0, seen1 = limit - j1;  // of each entry's keys
-      if (masked) mask_scores(s, seen0, seen1);
-      float top4[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        top4[q] = fmaxf(s[q][0], s[q][1]);
-#pragma unroll
-        for (int e = 2; e < 32; e += 2) top4[q] = max3(top4[q], s[q][e], s[q][e + 1]);
-      }
-      const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-      // moves the running maximum (and O and l with it) only when the row outgrows it
-      const bool move = top > m && (m == -INFINITY || (top - m) * scale2 > kLazy);
-      if (__any_sync(0xffffffffu, move)) {
-        const float to = move ? top : m;
-        const float f = m == -INFINITY ? 0.f : exp2_approx((m - to) * scale2);
-        l *= f;
-        if (t > 0) {
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tO + mine + 32 * q, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st_32(tO + mine + 32 * q, o);
-          }
-          // the scores are read again rather than held meanwhile
-          load_scores(tS + mine, s);
-          if (masked) mask_scores(s, seen0, seen1);
-        }
-        m = to;
-      }
-      const float shift = m == -INFINITY ? 0.f : -m * scale2;
-      const uint64_t scale22 = pair(scale2, scale2), shift2 = pair(shift, shift);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float u, v;
-          unpair(fma2(pair(s[q][2 * e], s[q][2 * e + 1]), scale22, shift2), u, v);
-          u = exp2_approx(u), v = exp2_approx(v);
-          sum[e & 1] = add2(sum[e & 1], pair(u, v));
-          p[e] = pack2<F16>(u, v);
-        }
-        tmem_st_16(tS + mine + 16 * q, p);
-      }
-      float l0, l1;
-      unpair(add2(sum[0], sum[1]), l0, l1);
-      l += l0 + l1;
-      // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
-      if (masked && (j0 + kBK > kl || (j1 < kl && j1 + kBK > kl))) {
-        ok = mbar_wait_bounded(bar(kVFull), ph, abort_flag, kErrWaitTma);
-        const int key = (r < kBK ? j0 : j1 - kBK) + r;  // this thread's row of the V tile
-        if (ok && key >= kl)
-          for (int d = 0; d < C::kHalves; ++d)
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(sp + C::kOffV + d * C::kHalf + r * 128 + 16 * e) =
-                  make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(kPFull));
-    }
-    if (tiles > 0 && __all_sync(0xffffffffu, ok))
-      ok = mbar_wait_bounded(bar(kOFull), 0, abort_flag, kErrWaitEpilogue);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    const float lse = l > 0.f ? (m * scale2 + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
-    const int64_t flat = (static_cast<int64_t>(b) * a.Hq + h) * a.Lq + row;
-    const bool write = r < rows && ok;
-    if (a.splits == 1 && write && a.lse) a.lse[flat] = lse;
-    const int64_t parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
-    if (a.splits > 1 && write) a.part[parts * D * a.splits + split * parts + flat] = lse;
-#pragma unroll
-    for (int q = 0; q < D / 32; ++q) {
-      uint32_t o[32];
-      if (tiles > 0) {
-        tmem_ld_32x32b_x32(tO + mine + 32 * q, o);
-        tmem_wait_ld();
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        o[e] = tiles > 0 && inv != 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-      if (write && a.splits > 1) {
-        uint4* dst = reinterpret_cast<uint4*>(a.part + (split * parts + flat) * D + 32 * q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-      } else if (write) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + b * a.o_batch +
-                                              row * a.o_row + h * a.o_head + 32 * q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = pack2<F16>(__uint_as_float(o[8 * e + 2 * k]),
-                              __uint_as_float(o[8 * e + 2 * k + 1]));
-          dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      __syncwarp();
-    }
-    tc_fence_before();
+    // the tensor memory is given back only when nothing writes it any more
+    const int drain = C::kDrain + (is_pv ? 1 : 0);
+    mma_commit(bar(drain));
+    mbar_wait_limit(bar(drain), 0, kWaitTimeoutNs, kErrWaitMma);
   }
   __syncwarp();
+  tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the parts of each row, in the order of the splits: a warp takes a row.
@@ -531,19 +739,22 @@ struct Plan {
   int splits, chunk;
 };
 
-// Few query blocks: the lists are cut so that the CTAs fill the GPU's 2 per SM once, in pieces of
-// at least two tiles; and in any case so that a piece fits a CTA's list.
+// The lists are cut (in pairs of entries) where that shortens the longest CTA's work: rounds of
+// items times the tiles of an item, of which about two more go to its beginning and end.
 inline Plan plan(int64_t B, int64_t Hq, int64_t Lq, int64_t T) {
-  const int64_t ctas = B * Hq * ((Lq + kBQ - 1) / kBQ);
-  int64_t splits = 2 * kSms / ctas;
-  const int64_t most = (T + 3) / 4, least = (T + kMaxList - 1) / kMaxList;
-  if (splits > most) splits = most;
-  if (splits < least) splits = least;
-  if (splits < 1) splits = 1;
-  int64_t chunk = (T + splits - 1) / splits;
-  chunk += chunk & 1;  // whole tiles
-  splits = (T + chunk - 1) / chunk;
-  return {static_cast<int>(splits), static_cast<int>(chunk)};
+  const int64_t items = B * Hq * ((Lq + kBQ - 1) / kBQ);
+  Plan best{1, static_cast<int>(T)};
+  if (items >= 4 * kSms) return best;
+  const int64_t tiles = (T + 1) / 2;
+  int64_t least = 0;
+  for (int64_t s = 1; s <= tiles && s <= 2 * kSms; ++s) {
+    const int64_t chunk = (tiles + s - 1) / s, splits = (tiles + chunk - 1) / chunk;
+    // a second kernel joins the parts: worth two tiles
+    const int64_t cost = (items * splits + kSms - 1) / kSms * (chunk + 2) + (splits > 1 ? 2 : 0);
+    if (s == 1 || cost < least)
+      least = cost, best = {static_cast<int>(splits), static_cast<int>(2 * chunk)};
+  }
+  return best;
 }
 
 // [B][H][L][D] view of 16-bit elements with strides in elements, as boxes of 64 columns.  A
@@ -570,12 +781,13 @@ inline bool make_map(CUtensorMap* map, const void* base, int64_t D, int64_t L, i
 
 template <int D, bool F16>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   const Args& a, cudaStream_t stream) {
+                   const Args& a, int sms, cudaStream_t stream) {
   auto kern = attn_kernel<D, F16>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Cfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(a.nq) * a.splits, a.Hq, a.B);
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hq * a.nq * a.splits;
+  const int grid = static_cast<int>(items < sms ? items : sms);
   kern<<<grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(q, k, v, a);
   const cudaError_t l = cudaGetLastError();
   if (l != cudaSuccess || a.splits == 1) return l;
