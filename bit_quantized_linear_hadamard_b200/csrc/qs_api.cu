@@ -1097,13 +1097,15 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
   }
   const int sms = qs::sm_count();
   if (sms <= 0) return QS_ERR_CUDA;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   if (!qs::attn::make_map(&mq, q, D, Lq, Hq, B, q_strides->row, q_strides->head, q_strides->batch,
                           QS_BLOCK_Q) ||
       !qs::attn::make_map(&mk, k, D, Lk, Hkv, B, k_strides->row, k_strides->head,
                           k_strides->batch, QS_BLOCK_K) ||
       !qs::attn::make_map(&mv, v, D, Lk, Hkv, B, v_strides->row, v_strides->head,
-                          v_strides->batch, QS_BLOCK_K))
+                          v_strides->batch, QS_BLOCK_K) ||
+      !qs::attn::make_map(&mo, out, D, Lq, Hq, B, out_strides->row, out_strides->head,
+                          out_strides->batch, QS_BLOCK_Q))
     return QS_ERR_CUDA;
   qs::attn::Args a{};
   a.out = out, a.o_batch = out_strides->batch, a.o_row = out_strides->row;
@@ -1119,8 +1121,8 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = dtype == QS_F16;
   const cudaError_t e =
-      D == 64 ? (f16 ? qs::attn::launch<64, true>(mq, mk, mv, a, sms, s) : qs::attn::launch<64, false>(mq, mk, mv, a, sms, s))
-              : (f16 ? qs::attn::launch<128, true>(mq, mk, mv, a, sms, s) : qs::attn::launch<128, false>(mq, mk, mv, a, sms, s));
+      D == 64 ? (f16 ? qs::attn::launch<64, true>(mq, mk, mv, mo, a, sms, s) : qs::attn::launch<64, false>(mq, mk, mv, mo, a, sms, s))
+              : (f16 ? qs::attn::launch<128, true>(mq, mk, mv, mo, a, sms, s) : qs::attn::launch<128, false>(mq, mk, mv, mo, a, sms, s));
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 

@@ -63,22 +63,27 @@ struct Cfg {
   static constexpr int kOffM = kOffV + kStages * kOp;              // running maxima, per group
   static constexpr int kOffMl = kOffM + kGroups * kBQ * 4;         // (m, l) per group, two items
   static constexpr int kOffTiles = kOffMl + 2 * kGroups * kBQ * 8; // first keys of a tile's blocks
-  static constexpr int kOffItems = kOffTiles + 8 * kTileRing;      // (item, tiles)
-  static constexpr int kOffBar = kOffItems + 8 * kItemRing;
+  static constexpr int kOffItems = kOffTiles + 8 * kTileRing;      // announced items
+  static constexpr int kOffBar = kOffItems + 32 * kItemRing;
   // barriers
   static constexpr int kKFull = 0, kKEmpty = kStages, kVFull = 2 * kStages, kVEmpty = 3 * kStages;
   static constexpr int kQFull = 4 * kStages, kQFree = kQFull + 2, kSFull = kQFree + 2;
-  static constexpr int kPFull = kSFull + kGroups, kPvDone = kPFull + kGroups;
-  static constexpr int kMReady = kPvDone + kGroups;  // per group and warp
-  static constexpr int kOFree = kMReady + kGroups * kGroupWarps, kTileFull = kOFree + 1;
+  static constexpr int kPFull = kSFull + kGroups;      // per group and half of the tile
+  static constexpr int kPvDone = kPFull + 2 * kGroups;
+  static constexpr int kMReady = kPvDone + kGroups;    // per group and warp
+  static constexpr int kMlFull = kMReady + kGroups * kGroupWarps;
+  static constexpr int kOFree = kMlFull + 1, kTileFull = kOFree + 1;
   static constexpr int kItemFull = kTileFull + kTileRing, kItemEmpty = kItemFull + kItemRing;
   static constexpr int kDrain = kItemEmpty + kItemRing, kNumBars = kDrain + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   __device__ static int arrivals(int i) {
-    if ((i >= kPFull && i < kPvDone) || i == kOFree) return i == kOFree ? kGroups * kGroupWarps : kGroupWarps;
-    if (i >= kItemEmpty && i < kDrain) return kGroups * kGroupWarps + 2;
+    const auto in = [&](int first, int n) { return i >= first && i < first + n; };
+    if (in(kPFull, 2 * kGroups)) return kGroupWarps;
+    if (i == kOFree || i == kMlFull) return kGroups * kGroupWarps;
+    if (in(kQFree, 2)) return 1 + kHalves;                        // scores formed, output staged
+    if (in(kItemEmpty, kItemRing)) return kGroups * kGroupWarps + 2;
     return 1;
   }
 };
@@ -241,88 +246,73 @@ __device__ __forceinline__ int checked_len(const int32_t* len, int b, int64_t mo
   return n;
 }
 
-// 64 scores of a row: those of one block.
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[64]) {
-  uint32_t r[2][32];
-  tmem_ld_32x32b_x32(taddr, r[0]);
-  tmem_ld_32x32b_x32(taddr + 32, r[1]);
-  tmem_wait_ld();
+// The scores of a row go through registers 32 at a time, in rolled loops: unrolled over the tile,
+// the three groups' code did not stay in the instruction caches and waited for its fetches.
+
+// -inf for the keys from `seen` on, which the row does not see.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], int seen) {
 #pragma unroll
-  for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(r[e / 32][e % 32]);
+  for (int e = 0; e < 32; ++e)
+    if (e >= seen) s[e] = 0xff800000u;
 }
 
-// -inf for the keys that the row does not see.
-__device__ __forceinline__ void mask_scores(float (&s)[64], int seen) {
+__device__ __forceinline__ float max32(const uint32_t (&s)[32], float top) {
+  float t[2] = {top, top};
 #pragma unroll
-  for (int e = 0; e < 64; ++e)
-    if (e >= seen) s[e] = -INFINITY;
-}
-
-__device__ __forceinline__ float max64(const float (&s)[64]) {
-  float top[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    top[q] = fmaxf(s[16 * q], s[16 * q + 1]);
-#pragma unroll
-    for (int e = 2; e < 16; e += 2) top[q] = max3(top[q], s[16 * q + e], s[16 * q + e + 1]);
+  for (int e = 0; e < 32; e += 4) {
+    t[0] = max3(t[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+    t[1] = max3(t[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
   }
-  return fmaxf(max3(top[0], top[1], top[2]), top[3]);
+  return max3(t[0], t[1], t[1]);
 }
 
-// P = exp2(scale2 * s + shift) of 64 scores into tensor memory; their sum is added to `sum`.
+// P = exp2(scale2 * s + shift) of 32 scores into tensor memory; their sum is added to `sum`.
 template <bool F16>
-__device__ __forceinline__ void exp_scores(uint32_t taddr, const float (&s)[64], uint64_t scale2,
-                                           uint64_t shift2, uint64_t (&sum)[2]) {
+__device__ __forceinline__ void exp32(uint32_t taddr, const uint32_t (&s)[32], uint64_t scale2,
+                                      uint64_t shift2, uint64_t (&sum)[2]) {
+  uint32_t p[16];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t p[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float u, v;
-      unpair(fma2(pair(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), scale2, shift2), u, v);
-      u = exp2_approx(u), v = exp2_approx(v);
-      sum[e & 1] = add2(sum[e & 1], pair(u, v));
-      p[e] = pack2<F16>(u, v);
-    }
-    tmem_st_16(taddr + 16 * q, p);
+  for (int e = 0; e < 16; ++e) {
+    float u, v;
+    unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale2, shift2), u,
+           v);
+    u = exp2_approx(u), v = exp2_approx(v);
+    sum[e & 1] = add2(sum[e & 1], pair(u, v));
+    p[e] = pack2<F16>(u, v);
   }
+  tmem_st_16(taddr, p);
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// One item: a range of the list of one query block.
-struct Item {
-  int b, h, hk, qb, split;
-  int ql, kl, row0, rows, off, seen;
-  const int32_t* list;
-  int len;  // entries of the range; 0 behind the sequence
+// One item: a range of the list of one query block.  The warp that reads the lists announces it
+// to the others through a ring in shared memory.
+struct alignas(16) Item {
+  int b, h, row0, split;
+  int ql, kl;  // lengths
+  int tiles;   // -1: no further item
+  int pad_;
 };
 
 __device__ __forceinline__ Item item_at(const Args& a, unsigned i) {
   Item it;
   it.split = static_cast<int>(i % static_cast<unsigned>(a.splits));
   i /= static_cast<unsigned>(a.splits);
-  it.qb = static_cast<int>(i % static_cast<unsigned>(a.nq));
+  it.row0 = static_cast<int>(i % static_cast<unsigned>(a.nq)) * kBQ;
   i /= static_cast<unsigned>(a.nq);
   it.h = static_cast<int>(i % static_cast<unsigned>(a.Hq));
   it.b = static_cast<int>(i / static_cast<unsigned>(a.Hq));
-  it.hk = it.h / (a.Hq / a.Hkv);
   it.ql = checked_len(a.q_len, it.b, a.Lq);
   it.kl = checked_len(a.k_len, it.b, a.Lk);
-  it.row0 = it.qb * kBQ;
-  it.rows = min(kBQ, it.ql - it.row0);  // <= 0 behind the sequence: such rows stay as they are
-  it.off = it.kl - it.ql;               // causal: row i sees keys up to i + off
-  it.seen = a.causal ? min(it.kl, it.row0 + it.rows + it.off) : it.kl;  // by the last row
-  it.list = a.blocks + ((static_cast<int64_t>(it.b) * a.Hq + it.h) * a.nq + it.qb) * a.T +
-            static_cast<int64_t>(it.split) * a.chunk;
-  it.len = it.rows > 0 ? min(a.chunk, a.T - it.split * a.chunk) : 0;
+  it.tiles = 0;
   return it;
 }
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const Args a) {
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                const Args a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -332,9 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* maxima = reinterpret_cast<float*>(sp + C::kOffM);  // [group][row]
   float2* ml = reinterpret_cast<float2*>(sp + C::kOffMl);   // [item parity][group][row]
   int2* tile_ring = reinterpret_cast<int2*>(sp + C::kOffTiles);
-  int2* item_ring = reinterpret_cast<int2*>(sp + C::kOffItems);
+  Item* item_ring = reinterpret_cast<Item*>(sp + C::kOffItems);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + C::kOffMisc + 4);
+  int* staged_warps = reinterpret_cast<int*>(sp + C::kOffMisc + 8);  // per 64 columns, modulo 4
   const auto bar = [&](int i) { return sbase + C::kOffBar + 8u * i; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -343,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kNumBars; ++i) mbar_init(bar(i), C::arrivals(i));
     *abort_flag = 0;
+    staged_warps[0] = staged_warps[1] = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -353,14 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmO);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // After a wait that gave up, every role runs through to its end without waiting or issuing
-  // anything more, so that all threads still meet at the barriers.
+  // After a wait that gave up, a thread waits for nothing more and leaves its loops; no barrier
+  // but the block's last one is unbounded.
   bool ok = true;
   const auto wait = [&](int i, uint32_t parity, unsigned err) {
     if (ok) ok = mbar_wait_bounded(bar(i), parity, abort_flag, err);
@@ -375,55 +368,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + kColS + kTileK * group + lanes, tO = tmem + kColO + lanes;
     const float scale2 = a.scale * kLog2e;
     const uint64_t scale22 = pair(scale2, scale2);
-    unsigned g0 = 0;    // tiles of the items so far
+    unsigned g0 = 0;      // tiles of the items so far
+    unsigned q_items = 0; // items with tiles
+    int staged = -1;      // Q buffer whose output store this thread has yet to see off
+    const auto see_off = [&] {
+      if (staged < 0) return;
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      mbar_arrive(bar(C::kQFree + staged));
+      staged = -1;
+    };
     for (unsigned e = 0;; ++e) {
       const int item_slot = e % kItemRing;
       wait(C::kItemFull + item_slot, (e / kItemRing) & 1, kErrWaitProducer);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const Item it = item_ring[item_slot];
       __syncwarp();
-      const int2 entry = item_ring[item_slot];
-      // an aborted block leaves together: the flag was up before any thread's wait gave up, but
-      // threads may differ on this wait, so all agree at the barrier below
-      const int leave = entry.x < 0 || !ok;
-      int any_leave;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-          "barrier.cta.red.or.pred q, 2, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-          : "=r"(any_leave)
-          : "r"(leave), "n"(32 * kTmaWarp)
-          : "memory");
-      if (any_leave) break;
       if (lane == 0) mbar_arrive(bar(C::kItemEmpty + item_slot));
-      const Item it = item_at(a, static_cast<unsigned>(entry.x));
-      const int n = entry.y;
+      const int n = it.tiles;
+      if (n < 0) break;
       const int row = it.row0 + r;
-      const int limit = a.causal ? min(it.kl, row + it.off + 1) : it.kl;    // keys this row sees
-      const int full = a.causal ? min(it.kl, it.row0 + it.off + 1) : it.kl; // keys every row sees
+      const int off = it.kl - it.ql;  // causal: row i sees keys up to i + off
+      const int limit = a.causal ? min(it.kl, row + off + 1) : it.kl;    // keys this row sees
+      const int full = a.causal ? min(it.kl, it.row0 + off + 1) : it.kl; // keys every row sees
       float m = -INFINITY, l = 0.f;
       // tiles of this group: those with (g0 + t) % 3 == group
       for (int t = (group + kGroups - static_cast<int>(g0 % kGroups)) % kGroups; t < n; t += kGroups) {
         const unsigned g = g0 + t;
         const uint32_t ph = (g / kGroups) & 1;
         wait(C::kTileFull + g % kTileRing, (g / kTileRing) & 1, kErrWaitProducer);
+        // the running maximum from the tile before, there before this tile's scores as a rule
+        const int from = (group + kGroups - 1) % kGroups;
+        if (t > 0)
+          wait(C::kMReady + from * kGroupWarps + quarter, ((g - 1) / kGroups) & 1, kErrWaitEpilogue);
+        __syncwarp();
+        const float old = t > 0 ? maxima[from * kBQ + r] : -INFINITY;
         wait(C::kSFull + group, ph, kErrWaitEpilogue);
         __syncwarp();
         tc_fence_after();
         const int2 tile = tile_ring[g % kTileRing];
         const bool masked = tile.x + kBK > full || tile.y + kBK > full;
-        float s[64];
-        load_scores(tS + kBK, s);
-        if (masked) mask_scores(s, limit - tile.y);
-        float top = max64(s);
-        load_scores(tS, s);
-        if (masked) mask_scores(s, limit - tile.x);
-        top = fmaxf(top, max64(s));
-        // the running maximum from the tile before; it moves only when the row outgrows it
-        float old = -INFINITY;
-        if (t > 0) {
-          const int from = (group + kGroups - 1) % kGroups;
-          wait(C::kMReady + from * kGroupWarps + quarter, ((g - 1) / kGroups) & 1, kErrWaitEpilogue);
-          __syncwarp();
-          old = maxima[from * kBQ + r];
+        // two sets of registers: the next 32 scores are on their way while these are looked at
+        uint32_t sa[32], sb[32];
+        float top = -INFINITY;
+        tmem_ld_32x32b_x32(tS, sa);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int seen = limit - (c == 0 ? tile.x : tile.y);
+          tmem_ld_32x32b_x32(tS + kBK * c + 32, sb);
+          if (masked) mask32(sa, seen);
+          top = max32(sa, top);
+          tmem_wait_ld();
+          tmem_ld_32x32b_x32(tS + kBK * (c ^ 1), sa);  // at the end: the first ones again
+          if (masked) mask32(sb, seen - 32);
+          top = max32(sb, top);
+          tmem_wait_ld();
         }
+        // it moves only when the row outgrows it
         const bool move = top > old && (old == -INFINITY || (top - old) * scale2 > kLazy);
         const float now = move ? top : old;
         maxima[group * kBQ + r] = now;
@@ -448,18 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = m == -INFINITY ? 0.f : l * exp2_approx((m - now) * scale2);
           m = now;
         }
-        const float shift = m == -INFINITY ? 0.f : -m * scale2;
-        const uint64_t shift2 = pair(shift, shift);
-        uint64_t sum[2] = {0ull, 0ull};
-        exp_scores<F16>(tS, s, scale22, shift2, sum);
-        load_scores(tS + kBK, s);
-        if (masked) mask_scores(s, limit - tile.y);
-        exp_scores<F16>(tS + kBK / 2, s, scale22, shift2, sum);
-        float l0, l1;
-        unpair(add2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
         // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
-        if (tile.x + kBK > it.kl || (tile.y < it.kl && tile.y + kBK > it.kl)) {
+        // (behind the tensor's end the copies have filled in zeros already)
+        if (it.kl < a.Lk &&
+            (tile.x + kBK > it.kl || (tile.y < it.kl && tile.y + kBK > it.kl))) {
           const int slot = static_cast<int>(g % C::kStages);
           wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
           const int key = r < kBK ? tile.x + r : tile.y + r - kBK;  // this thread's row of V
@@ -469,71 +462,149 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(sp + C::kOffV + slot * C::kOp + d * C::kHalf + r * 128 +
                                           16 * k) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
+          __syncwarp();
+          // both halves' products read rows that other warps of the group have cleared: each
+          // warp's arrival for the first half says that its rows are done
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::kPFull + group));
+        // P of a block goes to the second product as soon as it is written
+        const auto give_half = [&](int half) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kPFull + 2 * group + half));
+        };
+        const float shift = m == -INFINITY ? 0.f : -m * scale2;
+        const uint64_t shift2 = pair(shift, shift);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int seen = limit - (c == 0 ? tile.x : tile.y);
+          tmem_ld_32x32b_x32(tS + kBK * c + 32, sb);
+          if (masked) mask32(sa, seen);
+          exp32<F16>(tS + 32 * c, sa, scale22, shift2, sum);
+          tmem_wait_ld();
+          if (c == 0) tmem_ld_32x32b_x32(tS + kBK, sa);
+          if (masked) mask32(sb, seen - 32);
+          exp32<F16>(tS + 32 * c + 16, sb, scale22, shift2, sum);
+          tmem_wait_ld();
+          give_half(c);
+        }
+        float l0, l1;
+        unpair(add2(sum[0], sum[1]), l0, l1);
+        l += l0 + l1;
+        see_off();
       }
       g0 += n;
-      // the item's end: the groups' sums meet, then 32 columns of O at a time go to a group
+      see_off();  // the item after this one needs that buffer, wherever this thread then waits
+      // the item's end: the groups' sums meet.  The group of the last tile and the one before it
+      // write out 64 columns of O each (one of them, for D = 64); the third, whose tile is next,
+      // goes on.  The sums' slots alternate: all groups have read the item before the last when
+      // the last one's sums are complete.
+      if (e > 0) wait(C::kMlFull, (e - 1) & 1, kErrWaitEpilogue);
       ml[((e & 1) * kGroups + group) * kBQ + r] = make_float2(m, l);
-      asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kTmaWarp) : "memory");
-      if (n > 0) wait(C::kPvDone + (g0 - 1) % kGroups, ((g0 - 1) / kGroups) & 1, kErrWaitEpilogue);
       __syncwarp();
-      tc_fence_after();
-      float mm = -INFINITY, sum = 0.f;
+      if (lane == 0) mbar_arrive(bar(C::kMlFull));
+      const int last = static_cast<int>((g0 + kGroups - 1) % kGroups);  // any, for n == 0
+      const int half = (last + kGroups - group) % kGroups;
+      const int qb = q_items & 1;
+      q_items += n > 0;
+      if (half < C::kHalves) {
+        wait(C::kMlFull, e & 1, kErrWaitEpilogue);
+        if (n > 0) wait(C::kPvDone + last, ((g0 - 1) / kGroups) & 1, kErrWaitEpilogue);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k) mm = fmaxf(mm, ml[((e & 1) * kGroups + k) * kBQ + r].x);
-#pragma unroll
-      for (int k = 0; k < kGroups; ++k) {
-        const float2 v = ml[((e & 1) * kGroups + k) * kBQ + r];
-        if (v.x != -INFINITY) sum += v.y * exp2_approx((v.x - mm) * scale2);
-      }
-      // a sum of 0: no key seen; NaN goes on into the row
-      const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
-      const float lse = sum > 0.f ? (mm * scale2 + log2f(sum)) * kLn2 : (sum == sum ? -INFINITY : sum);
-      const int64_t flat = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Lq + row;
-      const int64_t parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
-      const bool write = r < it.rows && ok;
-      if (write && group == kGroups - 1) {
-        if (a.splits > 1)
-          a.part[parts * D * a.splits + it.split * parts + flat] = lse;
-        else if (a.lse)
-          a.lse[flat] = lse;
-      }
+        for (int k = 0; k < kGroups; ++k) mm = fmaxf(mm, ml[((e & 1) * kGroups + k) * kBQ + r].x);
 #pragma unroll 1
-      for (int q = group; q < D / 32; q += kGroups) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tO + 32 * q, o);
-        tmem_wait_ld();
+        for (int k = 0; k < kGroups; ++k) {
+          const float2 v = ml[((e & 1) * kGroups + k) * kBQ + r];
+          if (v.x != -INFINITY) sum += v.y * exp2_approx((v.x - mm) * scale2);
+        }
+        // a sum of 0: no key seen; NaN goes on into the row
+        const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
+        const int64_t flat = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Lq + row;
+        const int64_t parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
+        const bool write = row < it.ql;
+        // A whole block goes through shared memory (its Q is done with) and out by TMA: single
+        // rows from the threads would take 2048 line accesses of the L1.  The loop is kept short:
+        // code that runs once per item comes from beyond the instruction cache, and unrolled it
+        // took longer to fetch than to run.
+        const bool whole = n > 0 && it.row0 + kBQ <= it.ql && a.splits == 1;
+        uint8_t* stage = sp + C::kOffQ + qb * C::kOp + half * C::kHalf + r * 128;
+        uint16_t* direct = static_cast<uint16_t*>(a.out) + it.b * a.o_batch + row * a.o_row +
+                           it.h * a.o_head + 64 * half;
+        float* part = a.part + (it.split * parts + flat) * D + 64 * half;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[16];
+          tmem_ld_16(tO + 64 * half + 16 * k, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          o[k] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
-        if (write && a.splits > 1) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part + (it.split * parts + flat) * D + 32 * q);
+          for (int j = 0; j < 16; ++j)
+            o[j] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
+          if (a.splits > 1) {
+            if (write)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else if (write) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + it.b * a.o_batch +
-                                                row * a.o_row + it.h * a.o_head + 32 * q);
+              for (int j = 0; j < 4; ++j)
+                reinterpret_cast<uint4*>(part)[4 * k + j] =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = pack2<F16>(__uint_as_float(o[8 * k + 2 * j]),
-                                __uint_as_float(o[8 * k + 2 * j + 1]));
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 8; ++j)
+              o[j] = pack2<F16>(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
+            const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
+            if (whole) {
+              *reinterpret_cast<uint4*>(stage + 16 * ((2 * k) ^ (r & 7))) = lo;
+              *reinterpret_cast<uint4*>(stage + 16 * ((2 * k + 1) ^ (r & 7))) = hi;
+            } else if (write) {
+              reinterpret_cast<uint4*>(direct)[2 * k] = lo;
+              reinterpret_cast<uint4*>(direct)[2 * k + 1] = hi;
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        if (whole) fence_proxy_async_smem();
+        __syncwarp();
+        if (n > 0 && lane == 0) {
+          mbar_arrive(bar(C::kOFree));
+          // the last of the group's warps sends the 64 columns off, or gives the buffer back
+          __threadfence_block();
+          if ((atomicAdd(&staged_warps[half], 1) & (kGroupWarps - 1)) == kGroupWarps - 1) {
+            if (whole) {
+              __threadfence_block();
+              fence_proxy_async_smem();
+              see_off();
+              asm volatile(
+                  "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group"
+                  " [%0, {%1, %2, %3, %4}], [%5];\n\tcp.async.bulk.commit_group;" ::"l"(
+                      reinterpret_cast<uint64_t>(&tmO)),
+                  "r"(64 * half), "r"(it.row0), "r"(it.h), "r"(it.b),
+                  "r"(sbase + C::kOffQ + qb * C::kOp + half * C::kHalf)
+                  : "memory");
+              staged = qb;
+            } else {
+              mbar_arrive(bar(C::kQFree + qb));
+            }
           }
         }
+        if (write && half == 0) {
+          const float lse =
+              sum > 0.f ? (mm * scale2 + log2f(sum)) * kLn2 : (sum == sum ? -INFINITY : sum);
+          if (a.splits > 1)
+            a.part[parts * D * a.splits + it.split * parts + flat] = lse;
+          else if (a.lse)
+            a.lse[flat] = lse;
+        }
         __syncwarp();
+      } else {
+        if (n > 0 && lane == 0) mbar_arrive(bar(C::kOFree));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (n > 0 && lane == 0) mbar_arrive(bar(C::kOFree));
     }
+    see_off();
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == kTmaWarp || warp == kTmaVWarp) {
     // ---- the lists, and Q, K and V by TMA: one warp announces the items and loads Q and K, the
     // other V, as K is wanted up to three tiles before V.  The tiles of an item are pairs of its
@@ -544,34 +615,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = sbase + (is_v ? C::kOffV : C::kOffK);
     const int bar_full = is_v ? C::kVFull : C::kKFull, bar_empty = is_v ? C::kVEmpty : C::kKEmpty;
     unsigned g = 0, e = 0, loaded_q = 0, loaded = 0;
-    const auto list_part = [&](const Item& it, int i0, int& entry) {
-      entry = i0 + lane < it.len ? __ldg(it.list + i0 + lane) : -1;
+    struct List {
+      const int32_t* at;
+      int len, seen;  // entries of the item's range; keys that the block's last row sees
+    };
+    const auto list_of = [&](const Item& it) {
+      const int last = min(it.row0 + kBQ, it.ql) + it.kl - it.ql;
+      return List{a.blocks + ((static_cast<int64_t>(it.b) * a.Hq + it.h) * a.nq + it.row0 / kBQ) * a.T +
+                      static_cast<int64_t>(it.split) * a.chunk,
+                  min(a.chunk, a.T - it.split * a.chunk), a.causal ? min(it.kl, last) : it.kl};
+    };
+    const auto fetch = [&](const List& list, int i0) {
+      return i0 + lane < list.len ? __ldg(list.at + i0 + lane) : -1;
+    };
+    const auto steps = [&](const List& list, int entry) {
       const bool bad = entry < -1 || entry >= nk;
       if (bad) atomicOr(&g_error_word, kErrIndex);
-      return __ballot_sync(0xffffffffu, entry >= 0 && !bad && entry * kBK < it.seen);
+      return __ballot_sync(0xffffffffu, entry >= 0 && !bad && entry * kBK < list.seen);
     };
     const auto agree = [&] { ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0; };
-    const auto announce = [&](int item, int tiles) {
+    const auto announce = [&](const Item& it) {
       const int slot = e % kItemRing;
       if (lane == 0) {
         wait(C::kItemEmpty + slot, ((e / kItemRing) & 1) ^ 1, kErrWaitProducer);
-        item_ring[slot] = make_int2(item, tiles);
+        item_ring[slot] = it;
         mbar_arrive(bar(C::kItemFull + slot));
       }
       ++e;
       agree();
     };
-    for (unsigned i = blockIdx.x; i < items && ok; i += gridDim.x) {
-      const Item it = item_at(a, i);
-      if (it.rows <= 0) continue;
-      int entry;
+    // The item after the current one is looked up and its list counted bit by bit while the
+    // current one's tiles are loaded, never with a load from memory to wait for.
+    unsigned next = blockIdx.x;
+    Item nit;
+    List nlist{};
+    int n_count = 0, n_i0 = 0, n_first = -1, n_entry = -1;
+    const auto look_up = [&] {  // next: the next item with rows
+      for (; next < items; next += gridDim.x) {
+        nit = item_at(a, next);
+        if (nit.row0 >= nit.ql) continue;  // behind the sequence: such rows stay as they are
+        nlist = list_of(nit);
+        n_count = n_i0 = 0;
+        n_first = n_entry = fetch(nlist, 0);
+        break;
+      }
+    };
+    const auto count_part = [&] {
+      if (next >= items || n_i0 >= nlist.len) return;
+      n_count += __popc(steps(nlist, n_entry));
+      n_i0 += 32;
+      n_entry = fetch(nlist, n_i0);
+    };
+    look_up();
+    while (ok && next < items) {
+      if (!is_v)
+        while (n_i0 < nlist.len) count_part();
+      Item it = nit;
+      const List list = nlist;
+      int entry = n_first, ahead = 0;
+      next += gridDim.x;
       if (!is_v) {
-        int n = 0;
-        for (int i0 = 0; i0 < it.len; i0 += 32) n += __popc(list_part(it, i0, entry));
-        const int tiles = (n + 1) / 2;
-        announce(static_cast<int>(i), tiles);
-        if (tiles == 0) continue;
-        if (lane == 0) {
+        it.tiles = (n_count + 1) / 2;
+        announce(it);
+        if (lane == 0 && it.tiles > 0) {
           const int qb = loaded_q & 1;
           wait(C::kQFree + qb, ((loaded_q >> 1) & 1) ^ 1, kErrWaitProducer);
           if (ok) {
@@ -584,47 +690,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         agree();
       }
-      const int hc = it.hk * (is_v ? a.v_by_head : a.k_by_head);
+      const int hk = it.h / (a.Hq / a.Hkv);
+      const int hc = hk * (is_v ? a.v_by_head : a.k_by_head);
       const int bc = it.b * (is_v ? a.v_by_batch : a.k_by_batch);
-      const auto load_tile = [&](int j0, int j1) {  // lane 0
-        const int slot = static_cast<int>(g % C::kStages);
-        wait(bar_empty + slot, ((g / C::kStages) & 1) ^ 1, kErrWaitProducer);
-        if (!ok) return;
-        if (!is_v) {
-          // a missing second block: no key of it is seen, and it is loaded from behind the last
-          // key, as zeros
-          tile_ring[g % kTileRing] = make_int2(j0, j1 < a.Lk ? j1 : 0x40000000);
-          mbar_arrive(bar(C::kTileFull + g % kTileRing));
+      const auto load_tile = [&](int j0, int j1) {
+        if (lane == 0) {
+          const int slot = static_cast<int>(g % C::kStages);
+          wait(bar_empty + slot, ((g / C::kStages) & 1) ^ 1, kErrWaitProducer);
+          if (ok) {
+            if (!is_v) {
+              // a missing second block: no key of it is seen, and it is loaded from behind the
+              // last key, as zeros
+              tile_ring[g % kTileRing] = make_int2(j0, j1 < a.Lk ? j1 : 0x40000000);
+              mbar_arrive(bar(C::kTileFull + g % kTileRing));
+            }
+            const uint32_t full = bar(bar_full + slot), dst = ring + slot * C::kOp;
+            mbar_arrive_expect_tx(full, C::kOp);
+            for (int d = 0; d < C::kHalves; ++d) {
+              tma_load_4d(dst + d * C::kHalf, map, 64 * d, j0, hc, bc, full);
+              tma_load_4d(dst + d * C::kHalf + C::kHalf / 2, map, 64 * d, j1, hc, bc, full);
+            }
+            ++loaded;
+          }
         }
-        const uint32_t full = bar(bar_full + slot), dst = ring + slot * C::kOp;
-        mbar_arrive_expect_tx(full, C::kOp);
-        for (int d = 0; d < C::kHalves; ++d) {
-          tma_load_4d(dst + d * C::kHalf, map, 64 * d, j0, hc, bc, full);
-          tma_load_4d(dst + d * C::kHalf + C::kHalf / 2, map, 64 * d, j1, hc, bc, full);
-        }
-        ++loaded;
+        __syncwarp();
+        ++g;
+        if (++ahead == 2)
+          look_up();
+        else if (!is_v && ahead > 2)
+          count_part();
       };
       int first = -1;  // a tile's first block, waiting for its second
-      for (int i0 = 0; i0 < it.len && ok; i0 += 32) {
-        for (unsigned bits = list_part(it, i0, entry); bits; bits &= bits - 1) {
-          const int j = __shfl_sync(0xffffffffu, entry, __ffs(bits) - 1) * kBK;
+      for (int i0 = 0; i0 < list.len && ok; i0 += 32) {
+        const int now = entry;
+        entry = fetch(list, i0 + 32);
+        for (unsigned bits = steps(list, now); bits; bits &= bits - 1) {
+          const int j = __shfl_sync(0xffffffffu, now, __ffs(bits) - 1) * kBK;
           if (first < 0) {
             first = j;
-            continue;
+          } else {
+            load_tile(first, j);
+            first = -1;
           }
-          if (lane == 0) load_tile(first, j);
-          first = -1;
-          ++g;
         }
         agree();
       }
-      if (first >= 0) {
-        if (lane == 0) load_tile(first, static_cast<int>(a.Lk));
-        ++g;
-        agree();
-      }
+      if (first >= 0 && ok) load_tile(first, static_cast<int>(a.Lk));
+      if (ahead < 2) look_up();
+      agree();
     }
-    if (!is_v) announce(-1, 0);
+    if (!is_v) {
+      nit.tiles = -1;
+      announce(nit);
+    }
     // no copy into this CTA's memory may outlive it
     if (lane == 0) {
       for (unsigned k = loaded_q > 2 ? loaded_q - 2 : 0; k < loaded_q; ++k)
@@ -643,20 +761,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int item_slot = e % kItemRing;
       wait(C::kItemFull + item_slot, (e / kItemRing) & 1, kErrWaitMma);
       if (!ok) break;
-      const int2 entry = item_ring[item_slot];
+      const int n = item_ring[item_slot].tiles;
       mbar_arrive(bar(C::kItemEmpty + item_slot));
-      if (entry.x < 0) break;
-      if (entry.y == 0) continue;
+      if (n < 0) break;
+      if (n == 0) continue;
       const int qb = q & 1;
       if (!is_pv) {
         constexpr uint32_t idesc = idesc_f16(128, kTileK, F16, false);
         wait(C::kQFull + qb, (q >> 1) & 1, kErrWaitTma);
         const uint32_t aq = sbase + C::kOffQ + qb * C::kOp;
-        for (int t = 0; t < entry.y && ok; ++t, ++g) {
+        for (int t = 0; t < n && ok; ++t, ++g) {
           const int slot = static_cast<int>(g % C::kStages), buf = static_cast<int>(g % kGroups);
           // the buffer is free when P V of the tile three before is done
-          wait(C::kPvDone + buf, ((g / kGroups) & 1) ^ 1, kErrWaitMma);
           wait(C::kKFull + slot, (g / C::kStages) & 1, kErrWaitTma);
+          wait(C::kPvDone + buf, ((g / kGroups) & 1) ^ 1, kErrWaitMma);
           if (!ok) break;
           tc_fence_after();
           const uint32_t bk = sbase + C::kOffK + slot * C::kOp;
@@ -674,17 +792,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc = idesc_f16(128, D, F16, true);
         // O is free when the item before has been written out
         wait(C::kOFree, (q & 1) ^ 1, kErrWaitEpilogue);
-        for (int t = 0; t < entry.y && ok; ++t, ++g) {
+        for (int t = 0; t < n && ok; ++t, ++g) {
           const int slot = static_cast<int>(g % C::kStages), buf = static_cast<int>(g % kGroups);
-          wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
-          wait(C::kPFull + buf, (g / kGroups) & 1, kErrWaitMma);
-          if (!ok) break;
-          tc_fence_after();
           const uint32_t bv = sbase + C::kOffV + slot * C::kOp;
+          wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
 #pragma unroll
-          for (int s = 0; s < kTileK / 16; ++s)
-            mma_ts(tmem + kColO, tmem + kColS + kTileK * buf + 8 * s,
-                   smem_desc_mn(bv + s * 2048, C::kHalf), idesc, t != 0 || s != 0);
+          for (int half = 0; half < 2; ++half) {
+            wait(C::kPFull + 2 * buf + half, (g / kGroups) & 1, kErrWaitMma);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int s = half * kBK / 16; s < (half + 1) * kBK / 16; ++s)
+              mma_ts(tmem + kColO, tmem + kColS + kTileK * buf + 8 * s,
+                     smem_desc_mn(bv + s * 2048, C::kHalf), idesc, t != 0 || s != 0);
+          }
+          if (!ok) break;
           mma_commit(bar(C::kPvDone + buf));
           mma_commit(bar(C::kVEmpty + slot));
         }
@@ -781,14 +903,14 @@ inline bool make_map(CUtensorMap* map, const void* base, int64_t D, int64_t L, i
 
 template <int D, bool F16>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   const Args& a, int sms, cudaStream_t stream) {
+                   const CUtensorMap& o, const Args& a, int sms, cudaStream_t stream) {
   auto kern = attn_kernel<D, F16>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Cfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(a.B) * a.Hq * a.nq * a.splits;
   const int grid = static_cast<int>(items < sms ? items : sms);
-  kern<<<grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(q, k, v, a);
+  kern<<<grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(q, k, v, o, a);
   const cudaError_t l = cudaGetLastError();
   if (l != cudaSuccess || a.splits == 1) return l;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
