@@ -163,12 +163,12 @@ def _check(status: int, where: str) -> None:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without the objects around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -578,45 +578,49 @@ def qs_linear_gbs(x, M, K, alpha, w4_packed, w4_scale, w8_packed, w8_scale, bias
            "qs_linear_gbs")
 
 
-def _view(t, name, dtypes=(torch.bfloat16, torch.float16), dims=4):
-    """A CUDA view of `dims` dimensions whose last one is contiguous."""
+_16BIT = (torch.bfloat16, torch.float16)
+
+
+def _view(t, name, dtypes=_16BIT, dims=4):
+    """A CUDA view of `dims` dimensions whose last one is contiguous; its strides."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    st = t.stride()
+    if len(st) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(st)}")
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-
-
-def _strides(t):
-    return ctypes.byref(_Strides(t.stride(0), t.stride(1), t.stride(2)))
+    return st
 
 
 def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_ROPE_DTYPES = tuple(_DTYPES)
 
 
 def qs_rope(x, positions, inv_freq, y, pair_axis=None, scale=1.0, flags=0, stream=None):
     """x, y: [rows, heads, head_dim] views (y may be x); sizes and strides are theirs."""
-    _view(x, "x", tuple(_DTYPES), 3)
-    _view(y, "y", (x.dtype,), 3)
+    xs = _view(x, "x", _ROPE_DTYPES, 3)
+    ys = xs if y is x else _view(y, "y", (x.dtype,), 3)
     _shape(y, x.shape, "y")
     _cuda(positions, torch.int64, "positions")
     _cuda(inv_freq, torch.float64, "inv_freq")
     _cuda(pair_axis, torch.int32, "pair_axis")
     rows, heads, dim = x.shape
-    if positions.dim() not in (1, 2) or positions.shape[0] != rows:
+    ps = positions.shape
+    if len(ps) not in (1, 2) or ps[0] != rows:
         raise ValueError("positions must be [rows] or [rows, axes]")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot_dim / 2]")
     _shape(pair_axis, inv_freq.shape, "pair_axis")
-    _check(load().qs_rope(_p(x), x.stride(0), x.stride(1), rows, heads, dim, 2 * inv_freq.numel(),
-                          _p(positions), positions.shape[1] if positions.dim() == 2 else 1,
-                          _p(pair_axis), _p(inv_freq), float(scale), flags, _DTYPES[x.dtype], _p(y),
-                          y.stride(0), y.stride(1), _s(stream)), "qs_rope")
+    _check(load().qs_rope(_p(x), xs[0], xs[1], rows, heads, dim, 2 * inv_freq.numel(), _p(positions),
+                          ps[1] if len(ps) == 2 else 1, _p(pair_axis), _p(inv_freq), scale, flags,
+                          _DTYPES[x.dtype], _p(y), ys[0], ys[1], _s(stream)), "qs_rope")
 
 
 def qs_lora_workspace_bytes(M, K, R, requests) -> int:
@@ -638,13 +642,13 @@ def qs_lora_add(x, y, M, K, N, a, b, scale, adapters, R, seg_start, seg_adapter,
 
 def qs_block_means(x, lens, first_block, means, stream=None):
     """x: [B, L, H, D] view; means: float32 [B, H, ceil(L / 64), D]."""
-    _view(x, "x")
+    xs = _view(x, "x")
     B, L, H, D = x.shape
     _cuda(means, torch.float32, "means")
     _shape(means, (B, H, -(-L // QS_BLOCK_K), D), "means")
     _cuda(lens, torch.int32, "lens")
     _shape(lens, (B,), "lens")
-    _check(load().qs_block_means(_p(x), _strides(x), B, L, H, D, _DTYPES[x.dtype], _p(lens),
+    _check(load().qs_block_means(_p(x), _Strides(*xs[:3]), B, L, H, D, _DTYPES[x.dtype], _p(lens),
                                  first_block, _p(means), _s(stream)), "qs_block_means")
 
 
@@ -652,7 +656,7 @@ def qs_block_select(q, means, Lk, q_len, k_len, T, keep_first, keep_last, flags,
                     stream=None):
     """q: [B, Lq, Hq, D] view; means: float32 [B, Hkv, ceil(Lk / 64), D]; blocks: int32
     [B, Hq, ceil(Lq / 128), T]."""
-    _view(q, "q")
+    st = _view(q, "q")
     B, Lq, Hq, D = q.shape
     _cuda(means, torch.float32, "means")
     if means.dim() != 4:
@@ -662,11 +666,12 @@ def qs_block_select(q, means, Lk, q_len, k_len, T, keep_first, keep_last, flags,
     _cuda(blocks, torch.int32, "blocks")
     _shape(blocks, (B, Hq, -(-Lq // QS_BLOCK_Q), T), "blocks")
     for t, name in ((q_len, "q_len"), (k_len, "k_len")):
-        _cuda(t, torch.int32, name)
-        _shape(t, (B,), name)
-    _check(load().qs_block_select(_p(q), _strides(q), B, Lq, Hq, D, _DTYPES[q.dtype], _p(means), Lk,
-                                  Hkv, _p(q_len), _p(k_len), T, keep_first, keep_last, flags,
-                                  _p(blocks), _s(stream)), "qs_block_select")
+        if t is not None:
+            _cuda(t, torch.int32, name)
+            _shape(t, (B,), name)
+    _check(load().qs_block_select(_p(q), _Strides(*st[:3]), B, Lq, Hq, D, _DTYPES[q.dtype],
+                                  _p(means), Lk, Hkv, _p(q_len), _p(k_len), T, keep_first, keep_last,
+                                  flags, _p(blocks), _s(stream)), "qs_block_select")
 
 
 def qs_block_attention_workspace_bytes(B, Lq, Hq, D, T) -> int:
@@ -677,10 +682,9 @@ def qs_block_attention(q, k, v, blocks, q_len, k_len, scale, flags, workspace, o
                        stream=None):
     """q, out: [B, Lq, Hq, D], k, v: [B, Lk, Hkv, D] views; blocks: int32
     [B, Hq, ceil(Lq / 128), T]; lse: float32 [B, Hq, Lq] or None."""
-    _view(q, "q")
+    dtype = (q.dtype,)
+    qst, kst, vst, ost = _view(q, "q"), _view(k, "k", dtype), _view(v, "v", dtype), _view(out, "out", dtype)
     B, Lq, Hq, D = q.shape
-    for t, name in ((k, "k"), (v, "v"), (out, "out")):
-        _view(t, name, (q.dtype,))
     _, Lk, Hkv, _ = k.shape
     _shape(k, (B, Lk, Hkv, D), "k")
     _shape(v, k.shape, "v")
@@ -691,16 +695,18 @@ def qs_block_attention(q, k, v, blocks, q_len, k_len, scale, flags, workspace, o
     T = blocks.shape[3]
     _shape(blocks, (B, Hq, -(-Lq // QS_BLOCK_Q), T), "blocks")
     for t, name in ((q_len, "q_len"), (k_len, "k_len")):
-        _cuda(t, torch.int32, name)
-        _shape(t, (B,), name)
+        if t is not None:
+            _cuda(t, torch.int32, name)
+            _shape(t, (B,), name)
     _cuda(workspace, torch.uint8, "workspace")
     _cuda(lse, torch.float32, "lse")
     _shape(lse, (B, Hq, Lq), "lse")
-    _check(load().qs_block_attention(_p(q), _strides(q), _p(k), _strides(k), _p(v), _strides(v), B,
-                                     Lq, Lk, Hq, Hkv, D, _DTYPES[q.dtype], _p(blocks), T,
-                                     _p(q_len), _p(k_len), float(scale), flags, _p(workspace),
-                                     0 if workspace is None else workspace.numel(), _p(out),
-                                     _strides(out), _p(lse), _s(stream)), "qs_block_attention")
+    _check(load().qs_block_attention(_p(q), _Strides(*qst[:3]), _p(k), _Strides(*kst[:3]), _p(v),
+                                     _Strides(*vst[:3]), B, Lq, Lk, Hq, Hkv, D, _DTYPES[q.dtype],
+                                     _p(blocks), T, _p(q_len), _p(k_len), scale, flags,
+                                     _p(workspace), 0 if workspace is None else workspace.numel(),
+                                     _p(out), _Strides(*ost[:3]), _p(lse), _s(stream)),
+           "qs_block_attention")
 
 
 def qs_selftest_timeout(timeout_us: int, stream=None) -> None:
@@ -896,7 +902,7 @@ def rope(x, positions, inv_freq, pair_axis=None, interleaved: bool = True, scale
     ``inv_freq`` float64 [rot_dim/2] and ``pair_axis`` (`rope_frequencies`).  ``out`` may be x (in
     place); by default a new contiguous tensor."""
     if out is None:
-        _view(x, "x", tuple(_DTYPES), 3)
+        _view(x, "x", _ROPE_DTYPES, 3)
         out = _empty(x.shape, x.dtype, x.device, stream)
     flags = (QS_ROPE_INTERLEAVED if interleaved else 0) | (QS_ROPE_INVERSE if inverse else 0)
     qs_rope(x, positions, inv_freq, out, pair_axis, scale, flags, stream)

@@ -72,8 +72,8 @@ struct Cfg {
   static constexpr int kPvDone = kPFull + 2 * kGroups;
   static constexpr int kMReady = kPvDone + kGroups;    // per group and warp
   static constexpr int kMlFull = kMReady + kGroups * kGroupWarps;
-  static constexpr int kOFree = kMlFull + 1, kTileFull = kOFree + 1;
-  static constexpr int kItemFull = kTileFull + kTileRing, kItemEmpty = kItemFull + kItemRing;
+  static constexpr int kOFree = kMlFull + 1;
+  static constexpr int kItemFull = kOFree + 1, kItemEmpty = kItemFull + kItemRing;
   static constexpr int kDrain = kItemEmpty + kItemRing, kNumBars = kDrain + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
@@ -81,6 +81,7 @@ struct Cfg {
   __device__ static int arrivals(int i) {
     const auto in = [&](int first, int n) { return i >= first && i < first + n; };
     if (in(kPFull, 2 * kGroups)) return kGroupWarps;
+    if (in(kSFull, kGroups)) return 2;                            // formed, and its keys known
     if (i == kOFree || i == kMlFull) return kGroups * kGroupWarps;
     if (in(kQFree, 2)) return 1 + kHalves;                        // scores formed, output staged
     if (in(kItemEmpty, kItemRing)) return kGroups * kGroupWarps + 2;
@@ -395,10 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = (group + kGroups - static_cast<int>(g0 % kGroups)) % kGroups; t < n; t += kGroups) {
         const unsigned g = g0 + t;
         const uint32_t ph = (g / kGroups) & 1;
-        wait(C::kTileFull + g % kTileRing, (g / kTileRing) & 1, kErrWaitProducer);
         // the running maximum from the tile before, there before this tile's scores as a rule
         const int from = (group + kGroups - 1) % kGroups;
-        if (t > 0)
+        if (g > 0)
           wait(C::kMReady + from * kGroupWarps + quarter, ((g - 1) / kGroups) & 1, kErrWaitEpilogue);
         __syncwarp();
         const float old = t > 0 ? maxima[from * kBQ + r] : -INFINITY;
@@ -702,7 +702,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               // a missing second block: no key of it is seen, and it is loaded from behind the
               // last key, as zeros
               tile_ring[g % kTileRing] = make_int2(j0, j1 < a.Lk ? j1 : 0x40000000);
-              mbar_arrive(bar(C::kTileFull + g % kTileRing));
             }
             const uint32_t full = bar(bar_full + slot), dst = ring + slot * C::kOp;
             mbar_arrive_expect_tx(full, C::kOp);
@@ -784,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + kColS + kTileK * buf, smem_desc_sw128(aq + at), smem_desc_sw128(bk + at),
                    idesc, s != 0);
           }
+          mbar_arrive(bar(C::kSFull + buf));  // hands on the tile ring's entry, which came before K
           mma_commit(bar(C::kSFull + buf));
           mma_commit(bar(C::kKEmpty + slot));
         }
@@ -866,10 +866,10 @@ struct Plan {
 inline Plan plan(int64_t B, int64_t Hq, int64_t Lq, int64_t T) {
   const int64_t items = B * Hq * ((Lq + kBQ - 1) / kBQ);
   Plan best{1, static_cast<int>(T)};
-  if (items >= 4 * kSms) return best;
   const int64_t tiles = (T + 1) / 2;
   int64_t least = 0;
-  for (int64_t s = 1; s <= tiles && s <= 2 * kSms; ++s) {
+  const int64_t most = 1 + 2 * kSms / items;  // more than two items per CTA gain nothing
+  for (int64_t s = 1; s <= tiles && s <= most; ++s) {
     const int64_t chunk = (tiles + s - 1) / s, splits = (tiles + chunk - 1) / chunk;
     // a second kernel joins the parts: worth two tiles
     const int64_t cost = (items * splits + kSms - 1) / kSms * (chunk + 2) + (splits > 1 ? 2 : 0);
