@@ -12,9 +12,19 @@
 // request s owns the tile numbers from start[s] / BM + s on; as ceil(len / BM) <= (start + len) /
 // BM - start / BM + 1, the ranges do not meet, and M / BM + requests numbers cover them all.
 //
-// Operands go from global memory straight to mma fragments: a fragment only needs A and B to use
-// the same order of k, so a thread takes 8 consecutive k (16 bytes) of a 32-wide slice for two
-// k16 steps, and the four threads of a row read 64 consecutive bytes.
+// Both are bound by HBM: x once, y and out once.
+//
+// Shrink, tiles of 128 rows (requests of 64 rows and more on average): tcgen05 MMAs of 128 x R on
+// a ring of TMA stages of 64 k; two CTAs per SM keep 190 KB in flight.  Tiles of 16 rows (a token
+// or a few per request): mma.sync, the block's warps share K, operands from global memory straight
+// to fragments.  A fragment only needs A and B to use the same order of k, so a thread takes 8
+// consecutive k (16 bytes) of a 32-wide slice for two k16 steps, and the four threads of a row
+// read 64 consecutive bytes.
+//
+// Expand: the same fragments.  Large tiles: a warp holds its 32 columns of B in registers and goes
+// down the rows, t comes from shared memory, y from two row groups ahead; with B read for every row
+// group instead the L1's line accesses bound it (2.1 TB/s against 6 now).  Small tiles: a warp holds
+// t and goes along the columns.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,6 +32,7 @@
 #include <cstdint>
 
 #include "qs.h"
+#include "qs_host.cuh"
 #include "qs_ptx.cuh"
 
 namespace qs {
@@ -33,6 +44,7 @@ constexpr int kSmallRows = 16, kLargeRows = 128;  // rows of a tile
 constexpr int kMaxRank = 128;
 constexpr int kGroup = 64;                        // ranks a shrink block forms
 constexpr int kSms = 148;
+constexpr int kStepK = 64;                        // k of a TMA stage
 
 struct Args {
   const uint16_t *x, *y, *a, *b;
@@ -55,10 +67,12 @@ inline Plan plan(int64_t M, int64_t K, int64_t R, int64_t requests) {
   p.large = M / requests >= kLargeRows / 2;
   const int rows = p.large ? kLargeRows : kSmallRows;
   p.tiles = M / rows + requests;
-  const int64_t blocks = p.tiles * ((R + kGroup - 1) / kGroup) * (p.large ? kLargeRows / 32 : 1);
-  int64_t s = (2 * kSms + blocks - 1) / blocks;
-  const int64_t most = K / 512 > 0 ? K / 512 : 1;  // 64 k and more for each warp
-  p.slices = static_cast<int>(s < 1 ? 1 : s > most ? most : s);
+  const int64_t blocks = p.large ? p.tiles : p.tiles * ((R + kGroup - 1) / kGroup);
+  // about two blocks per SM; small tiles: 64 k and more for each warp, large ones: 16 stages
+  int64_t n = 2 * kSms / blocks;
+  const int64_t most = p.large ? K / (16 * kStepK) : K / 512;
+  if (n > most) n = most;
+  p.slices = static_cast<int>(n < 1 ? 1 : n);
   return p;
 }
 
@@ -69,7 +83,7 @@ struct Tile {
 // The tile of number t; called by all threads of the block.
 __device__ __forceinline__ Tile find_tile(const Args& a, int64_t t, int bm) {
   int s;
-  if (a.requests <= kThreads) {
+  if (a.requests <= static_cast<int>(blockDim.x)) {
     // the ranges' first numbers grow with the request: count those not above t
     const int i = threadIdx.x;
     s = __syncthreads_count(i < a.requests && a.start[i] / bm + static_cast<int64_t>(i) <= t) - 1;
@@ -110,205 +124,447 @@ __device__ __forceinline__ uint4 ldg16(const uint16_t* p) {
   return __ldg(reinterpret_cast<const uint4*>(p));
 }
 
-// t: a block forms 16 * MT rows x up to 64 ranks (NT groups of 8) over one slice of K; its warps
-// share the slice's 32-wide steps and add their sums through shared memory in warp order.
-template <int MT, int NT>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const Args a, int bm) {
-  extern __shared__ float sums[];  // [warps][16 * MT][8 * NT]
-  const int sub = bm / (16 * MT);  // blocks per tile
-  const Tile tile = find_tile(a, blockIdx.x / sub, bm);
-  const int skip = (blockIdx.x % sub) * 16 * MT;
-  const int rows = min(tile.rows - skip, 16 * MT);
-  if (rows <= 0 || tile.adapter < 0) return;
-  const int row0 = tile.row0 + skip;
+// The second kernel may be on the GPU before the first has ended (programmatic dependent launch).
+// It waits for that end before it reads the sums, and every block of it does so before it leaves:
+// what comes after it in the stream must find both done.
+__device__ __forceinline__ void let_expand_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_shrink() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// t of a small tile: a block forms 16 rows x up to 64 ranks (NT groups of 8) over one slice of K;
+// its warps share the slice's 32-wide steps and add their sums through shared memory in warp order.
+template <int NT>
+__global__ void __launch_bounds__(kThreads) shrink_small_kernel(const Args a) {
+  extern __shared__ float sums[];  // [warps][16][8 * NT]
+  const Tile tile = find_tile(a, blockIdx.x, kSmallRows);
+  let_expand_start();
+  if (tile.rows <= 0 || tile.adapter < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int r0 = blockIdx.z * kGroup;
   const int steps = a.K / 32, parts = a.slices * kWarps, part = blockIdx.y * kWarps + warp;
   const int k_begin = static_cast<int>(static_cast<int64_t>(steps) * part / parts) * 32;
   const int k_end = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / parts) * 32;
 
-  float acc[MT][NT][4] = {};
-  const uint16_t* xp = a.x + static_cast<int64_t>(row0 + g) * a.K + 8 * c;
+  float acc[NT][4] = {};
+  const uint16_t* xp = a.x + static_cast<int64_t>(tile.row0 + g) * a.K + 8 * c;
   const uint16_t* ap =
       a.a + (static_cast<int64_t>(tile.adapter) * a.R + r0 + g) * a.K + 8 * c;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
+#pragma unroll 4
   for (int k = k_begin; k < k_end; k += 32) {
-    uint4 xf[MT][2], wf[NT];
+    uint4 xf[2], wf[NT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        xf[m][h] = 16 * m + 8 * h + g < rows
-                       ? ldg16(xp + static_cast<int64_t>(16 * m + 8 * h) * a.K + k)
-                       : zero;
+    for (int h = 0; h < 2; ++h)
+      xf[h] = 8 * h + g < tile.rows ? ldg16(xp + static_cast<int64_t>(8 * h) * a.K + k) : zero;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       wf[n] = r0 + 8 * n < a.R ? ldg16(ap + static_cast<int64_t>(8 * n) * a.K + k) : zero;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma_bf16_16816(acc[m][n], xf[m][0].x, xf[m][1].x, xf[m][0].y, xf[m][1].y, wf[n].x,
-                       wf[n].y);
-        mma_bf16_16816(acc[m][n], xf[m][0].z, xf[m][1].z, xf[m][0].w, xf[m][1].w, wf[n].z,
-                       wf[n].w);
-      }
+    for (int n = 0; n < NT; ++n) {
+      mma_bf16_16816(acc[n], xf[0].x, xf[1].x, xf[0].y, xf[1].y, wf[n].x, wf[n].y);
+      mma_bf16_16816(acc[n], xf[0].z, xf[1].z, xf[0].w, xf[1].w, wf[n].z, wf[n].w);
+    }
   }
   constexpr int cols = 8 * NT;
-  float* mine = sums + warp * (16 * MT * cols);
+  float* mine = sums + warp * (16 * cols);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        mine[(16 * m + g + 8 * (e >> 1)) * cols + 8 * n + 2 * c + (e & 1)] = acc[m][n][e];
+    for (int e = 0; e < 4; ++e)
+      mine[(g + 8 * (e >> 1)) * cols + 8 * n + 2 * c + (e & 1)] = acc[n][e];
   __syncthreads();
-  float* part_out = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + row0) * a.R + r0;
-  for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
+  float* out = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + tile.row0) * a.R + r0;
+  for (int i = threadIdx.x; i < tile.rows * cols; i += kThreads) {
     const int r = i % cols;
     if (r0 + r >= a.R) continue;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sums[w * (16 * MT * cols) + i];
-    part_out[static_cast<int64_t>(i / cols) * a.R + r] = v;
+    for (int w = 0; w < kWarps; ++w) v += sums[w * (16 * cols) + i];
+    out[static_cast<int64_t>(i / cols) * a.R + r] = v;
   }
 }
 
-// out = y + t B: a warp takes 16 rows and 32 columns at a time.  LARGE: the block's warps take
-// different rows and the same columns (B then comes from L1 for 7 of the 8); else the same 16 rows
-// and different columns.  KS: 32-wide steps of the rank.
-// The column order inside the 32 is permuted so that a thread's four n8 tiles hold 8 consecutive
-// columns: y and out move in 16-byte pieces.
-template <bool LARGE, int KS>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const Args a, int cols_per_block) {
-  const int bm = LARGE ? kLargeRows : kSmallRows;
-  const Tile tile = find_tile(a, blockIdx.x, bm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int skip = LARGE ? 16 * warp : 0;
-  const int rows = min(tile.rows - skip, 16);
-  if (rows <= 0) return;
-  const int64_t row0 = tile.row0 + skip;
-  const int n_end = min(a.N, (static_cast<int>(blockIdx.y) + 1) * cols_per_block);
-  const int n_begin = blockIdx.y * cols_per_block + (LARGE ? 0 : 32 * warp);
-  constexpr int n_step = LARGE ? 32 : 32 * kWarps;
-  const bool turned = tile.adapter >= 0;
-  if (!turned && a.out == a.y) return;
+// t of a large tile: x rows (whoever's they are behind the request: their results are not
+// written) times the adapter's R rows of A, one slice of K.  Warp 0 loads, warp 1 issues, warps
+// 2-5 carry the sums from tensor memory to the workspace.
+template <int RN>  // R rounded up to 16 (an MMA's columns): the rows loaded
+struct ShrinkCfg {
+  static constexpr int kX = kLargeRows * 128, kA = RN * 128, kStage = kX + kA;
+  static constexpr int kStages = 100 * 1024 / kStage;  // two CTAs per SM
+  static constexpr int kOffBar = kStages * kStage, kNumBars = 2 * kStages + 1;
+  static constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 16 + 1024;
+  static constexpr int kTmemCols = RN <= 32 ? 32 : RN <= 64 ? 64 : 128;
+  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+};
+constexpr int kShrinkThreads = 32 * 6;
 
-  uint32_t hi[KS][2][4], lo[KS][2][4];  // [step][row half][pairs of k]
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int RN>
+__global__ void __launch_bounds__(kShrinkThreads)
+    shrink_large_kernel(const __grid_constant__ CUtensorMap tmX,
+                        const __grid_constant__ CUtensorMap tmA, const Args a) {
+  using C = ShrinkCfg<RN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  uint8_t* sp = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + C::kOffBar + 8 * C::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const auto full = [&](int s) { return sbase + C::kOffBar + 8u * s; };
+  const auto empty = [&](int s) { return full(C::kStages + s); };
+  const uint32_t done = full(2 * C::kStages);
+  const Tile tile = find_tile(a, blockIdx.x, kLargeRows);
+  if (tile.rows <= 0 || tile.adapter < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int steps = a.K / kStepK;
+  const int k0 = static_cast<int>(static_cast<int64_t>(steps) * blockIdx.y / a.slices);
+  const int n = static_cast<int>(static_cast<int64_t>(steps) * (blockIdx.y + 1) / a.slices) - k0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) mbar_init(full(i), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  let_expand_start();
+
+  if (warp == 0 && lane == 0) {
+    int i = 0;
+    for (; i < n; ++i) {
+      const int s = i % C::kStages;
+      if (!mbar_wait_bounded(empty(s), ((i / C::kStages) & 1) ^ 1, abort_flag, kErrWaitProducer))
+        break;
+      const uint32_t dst = sbase + s * C::kStage;
+      mbar_arrive_expect_tx(full(s), C::kStage);
+      tma_load_2d(dst, &tmX, (k0 + i) * kStepK, tile.row0, full(s));
+      tma_load_2d(dst + C::kX, &tmA, (k0 + i) * kStepK, tile.adapter * a.R, full(s));
+    }
+    // no copy into this CTA's memory may outlive it
+    for (int k = i > C::kStages ? i - C::kStages : 0; k < i; ++k)
+      mbar_wait_limit(full(k % C::kStages), (k / C::kStages) & 1, kWaitTimeoutNs, kErrWaitTma);
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |  // binary32 D, bf16 A and B
+                               (static_cast<uint32_t>(RN >> 3) << 17) |
+                               (static_cast<uint32_t>(kLargeRows >> 4) << 24);
+    for (int i = 0; i < n; ++i) {
+      const int s = i % C::kStages;
+      if (!mbar_wait_bounded(full(s), (i / C::kStages) & 1, abort_flag, kErrWaitTma)) break;
+      tc_fence_after();
+      const uint32_t x = sbase + s * C::kStage;
+#pragma unroll
+      for (int k = 0; k < kStepK / 16; ++k)
+        mma_bf16_ss(tmem, smem_desc_sw128(x + 32 * k), smem_desc_sw128(x + C::kX + 32 * k), idesc,
+                    i != 0 || k != 0);
+      mma_commit(empty(s));
+    }
+    mma_commit(done);
+    mbar_wait_limit(done, 0, kWaitTimeoutNs, kErrWaitMma);
+  } else if (warp >= 2) {
+    const bool ok = mbar_wait_bounded(done, 0, abort_flag, kErrWaitMma);
+    __syncwarp();
+    tc_fence_after();
+    const int quarter = warp & 3, r = 32 * quarter + lane;  // the lanes of tensor memory it may read
+    float* out = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + tile.row0 + r) * a.R;
+#pragma unroll 1
+    for (int c = 0; c < C::kTmemCols / 32; ++c) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 32 * c, v);
+      tmem_wait_ld();
+      if (r < tile.rows && ok)
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          if (32 * c + e < a.R)  // R is a multiple of 8
+            *reinterpret_cast<uint4*>(out + 32 * c + e) =
+                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      __syncwarp();
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// Eight consecutive ranks of a row of t, scaled, as two bf16 numbers each: their tops and the rest.
+__device__ __forceinline__ void load_t(const Args& a, int64_t row, int k, float scale, bool there,
+                                       uint4& hi, uint4& lo) {
+  float t[8] = {};
+  if (there && k < a.R) {
+    const float* p = a.part + row * a.R + k;
+    for (int i = 0; i < a.slices; ++i, p += a.M * a.R) {
+      const float4 u = *reinterpret_cast<const float4*>(p);
+      const float4 v = *reinterpret_cast<const float4*>(p + 4);
+      t[0] += u.x, t[1] += u.y, t[2] += u.z, t[3] += u.w;
+      t[4] += v.x, t[5] += v.y, t[6] += v.z, t[7] += v.w;
+    }
+  }
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float p = t[2 * e] * scale, q = t[2 * e + 1] * scale;
+    const __nv_bfloat162 top = __floats2bfloat162_rn(p, q);
+    const float u = __low2float(top), v = __high2float(top);
+    // an infinite t stays infinite: its remainder is 0, not inf - inf
+    const __nv_bfloat162 rest =
+        __floats2bfloat162_rn(isinf(u) ? 0.f : p - u, isinf(v) ? 0.f : q - v);
+    h[e] = *reinterpret_cast<const uint32_t*>(&top);
+    l[e] = *reinterpret_cast<const uint32_t*>(&rest);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Two k16 steps of 16 rows x 8 columns: t as tops and rest, rows g (0) and g + 8 (1) of each.
+__device__ __forceinline__ void mma_t(float (&acc)[4], const uint4 (&hi)[2], const uint4 (&lo)[2],
+                                      const uint4& w) {
+  mma_bf16_16816(acc, hi[0].x, hi[1].x, hi[0].y, hi[1].y, w.x, w.y);
+  mma_bf16_16816(acc, lo[0].x, lo[1].x, lo[0].y, lo[1].y, w.x, w.y);
+  mma_bf16_16816(acc, hi[0].z, hi[1].z, hi[0].w, hi[1].w, w.z, w.w);
+  mma_bf16_16816(acc, lo[0].z, lo[1].z, lo[0].w, lo[1].w, w.z, w.w);
+}
+
+// y + the sums of four n8 tiles, as bf16.  The tiles' column order inside their 32 is permuted so
+// that a thread's share is 8 consecutive columns: y and out move in 16-byte pieces.
+__device__ __forceinline__ uint4 add_y(const uint4& y, const float (&acc)[4][4], int half) {
+  const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float u = __uint_as_float(yw[j] << 16), v = __uint_as_float(yw[j] & 0xFFFF0000u);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(u + acc[j][2 * half], v + acc[j][2 * half + 1]);
+    o[j] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// B of 32 columns: rank group s, tile j, in the permuted order.
+template <int KS>
+__device__ __forceinline__ void load_b(const Args& a, int adapter, int n0, uint4 (&w)[KS][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int s = 0; s < KS; ++s)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float t[8] = {};
-      const int k = 32 * s + 8 * c;
-      if (turned && k < a.R && g + 8 * h < rows) {
-        const float* p = a.part + (row0 + g + 8 * h) * a.R + k;
-        for (int i = 0; i < a.slices; ++i, p += a.M * a.R) {
-          const float4 u = *reinterpret_cast<const float4*>(p);
-          const float4 v = *reinterpret_cast<const float4*>(p + 4);
-          t[0] += u.x, t[1] += u.y, t[2] += u.z, t[3] += u.w;
-          t[4] += v.x, t[5] += v.y, t[6] += v.z, t[7] += v.w;
-        }
-        const float sc = a.scale ? a.scale[tile.adapter] : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] *= sc;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 top = __floats2bfloat162_rn(t[2 * e], t[2 * e + 1]);
-        const float u = __low2float(top), v = __high2float(top);
-        // an infinite t stays infinite: its remainder is 0, not inf - inf
-        const __nv_bfloat162 rest =
-            __floats2bfloat162_rn(isinf(u) ? 0.f : t[2 * e] - u, isinf(v) ? 0.f : t[2 * e + 1] - v);
-        hi[s][h][e] = *reinterpret_cast<const uint32_t*>(&top);
-        lo[s][h][e] = *reinterpret_cast<const uint32_t*>(&rest);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int k = 32 * s + 8 * c, n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
+      w[s][j] = k < a.R && n < a.N
+                    ? ldg16(a.b + (static_cast<int64_t>(adapter) * a.N + n) * a.R + k)
+                    : make_uint4(0, 0, 0, 0);
     }
+}
 
+// Large tiles.  KS: 32-wide steps of the rank.
+template <int KS>
+__global__ void __launch_bounds__(kThreads, KS <= 2 ? 2 : 1) expand_large_kernel(const Args a) {
+  // rows of t: tops and rest, padded so that two rows 8 threads read lie in different banks
+  constexpr int kStride = 64 * KS + (KS % 2 == 0 ? 64 : 0), kRowGroups = kLargeRows / 16;
+  extern __shared__ __align__(16) uint8_t t_smem[];
+  const Tile tile = find_tile(a, blockIdx.x, kLargeRows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const bool turned = tile.adapter >= 0;
+  if (tile.rows <= 0 || (!turned && a.out == a.y)) {
+    wait_for_shrink();
+    return;
+  }
+  const int n0 = 32 * (blockIdx.y * kWarps + warp);
+  const bool in = n0 + 8 * c < a.N;  // N is a multiple of 16, a warp's columns are 32
+  uint4 w[KS][4];
+  if (turned) load_b<KS>(a, tile.adapter, n0, w);
+  const int64_t at = static_cast<int64_t>(tile.row0 + g) * a.N + n0 + 8 * c;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int n0 = n_begin; n0 < n_end; n0 += n_step) {
-    float acc[4][4] = {};
-    const bool in = n0 + 8 * c < a.N;  // N is a multiple of 16, a warp's columns are 32
-    uint4 yv[2];
+  const auto load_y = [&](int rg, int h) {
+    const int r = 16 * rg + 8 * h;
+    return in && r + g < tile.rows
+               ? *reinterpret_cast<const uint4*>(a.y + at + static_cast<int64_t>(r) * a.N)
+               : zero;
+  };
+  uint4 y[3][2];  // of this row group and the next two
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      yv[h] = in && g + 8 * h < rows
-                  ? *reinterpret_cast<const uint4*>(a.y + (row0 + g + 8 * h) * a.N + n0 + 8 * c)
-                  : zero;
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) y[d][h] = load_y(d, h);
+  wait_for_shrink();
+  if (turned) {
+    const float scale = a.scale ? a.scale[tile.adapter] : 1.f;
+    for (int i = threadIdx.x; i < kLargeRows * 4 * KS; i += kThreads) {
+      const int r = i / (4 * KS), k = 8 * (i % (4 * KS));
+      uint4 hi, lo;
+      load_t(a, tile.row0 + r, k, scale, r < tile.rows, hi, lo);
+      *reinterpret_cast<uint4*>(t_smem + r * kStride + 2 * k) = hi;
+      *reinterpret_cast<uint4*>(t_smem + (kLargeRows + r) * kStride + 2 * k) = lo;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int rg = 0; rg < kRowGroups; ++rg) {
+    if (16 * rg >= tile.rows) break;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) y[(rg + 2) % 3][h] = rg + 2 < kRowGroups ? load_y(rg + 2, h) : zero;
+    float acc[4][4] = {};
     if (turned) {
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const int k = 32 * s + 8 * c;
+        uint4 hi[2], lo[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-          const uint4 w =
-              k < a.R && n < a.N
-                  ? ldg16(a.b + (static_cast<int64_t>(tile.adapter) * a.N + n) * a.R + k)
-                  : zero;
-          mma_bf16_16816(acc[j], hi[s][0][0], hi[s][1][0], hi[s][0][1], hi[s][1][1], w.x, w.y);
-          mma_bf16_16816(acc[j], lo[s][0][0], lo[s][1][0], lo[s][0][1], lo[s][1][1], w.x, w.y);
-          mma_bf16_16816(acc[j], hi[s][0][2], hi[s][1][2], hi[s][0][3], hi[s][1][3], w.z, w.w);
-          mma_bf16_16816(acc[j], lo[s][0][2], lo[s][1][2], lo[s][0][3], lo[s][1][3], w.z, w.w);
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* p = t_smem + (16 * rg + 8 * h + g) * kStride + 64 * s + 16 * c;
+          hi[h] = *reinterpret_cast<const uint4*>(p);
+          lo[h] = *reinterpret_cast<const uint4*>(p + kLargeRows * kStride);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_t(acc[j], hi, lo, w[s][j]);
       }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!in || g + 8 * h >= rows) continue;
-      const uint32_t yw[4] = {yv[h].x, yv[h].y, yv[h].z, yv[h].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float u = __uint_as_float(yw[j] << 16), v = __uint_as_float(yw[j] & 0xFFFF0000u);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(u + acc[j][2 * h], v + acc[j][2 * h + 1]);
-        o[j] = turned ? *reinterpret_cast<const uint32_t*>(&r) : yw[j];
-      }
-      *reinterpret_cast<uint4*>(a.out + (row0 + g + 8 * h) * a.N + n0 + 8 * c) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+      const int r = 16 * rg + 8 * h;
+      if (!in || r + g >= tile.rows) continue;
+      *reinterpret_cast<uint4*>(a.out + at + static_cast<int64_t>(r) * a.N) =
+          turned ? add_y(y[rg % 3][h], acc, h) : y[rg % 3][h];
     }
+  }
+}
+
+// Small tiles: the warp's t in registers, 32 columns at a time.
+template <int KS>
+__global__ void __launch_bounds__(kThreads) expand_small_kernel(const Args a, int cols_per_block) {
+  const Tile tile = find_tile(a, blockIdx.x, kSmallRows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const bool turned = tile.adapter >= 0;
+  wait_for_shrink();
+  if (tile.rows <= 0 || (!turned && a.out == a.y)) return;
+  const int n_begin = blockIdx.y * cols_per_block + 32 * warp;
+  const int n_end = min(a.N, (static_cast<int>(blockIdx.y) + 1) * cols_per_block);
+  uint4 hi[KS][2], lo[KS][2];
+  const float scale = turned && a.scale ? a.scale[tile.adapter] : 1.f;
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      load_t(a, tile.row0 + g + 8 * h, 32 * s + 8 * c, scale, turned && g + 8 * h < tile.rows,
+             hi[s][h], lo[s][h]);
+#pragma unroll 2
+  for (int n0 = n_begin; n0 < n_end; n0 += 32 * kWarps) {
+    const bool in = n0 + 8 * c < a.N;
+    const int64_t at = static_cast<int64_t>(tile.row0 + g) * a.N + n0 + 8 * c;
+    uint4 y[2], w[KS][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      y[h] = in && g + 8 * h < tile.rows
+                 ? *reinterpret_cast<const uint4*>(a.y + at + static_cast<int64_t>(8 * h) * a.N)
+                 : make_uint4(0, 0, 0, 0);
+    float acc[4][4] = {};
+    if (turned) {
+      load_b<KS>(a, tile.adapter, n0, w);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_t(acc[j], hi[s], lo[s], w[s][j]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (in && g + 8 * h < tile.rows)
+        *reinterpret_cast<uint4*>(a.out + at + static_cast<int64_t>(8 * h) * a.N) =
+            turned ? add_y(y[h], acc, h) : y[h];
   }
 }
 
 template <int NT>
-cudaError_t launch_shrink(const Args& a, const Plan& p, cudaStream_t stream) {
-  const int groups = (a.R + kGroup - 1) / kGroup;
-  const int MT = p.large ? 2 : 1, bm = p.large ? kLargeRows : kSmallRows;
-  const dim3 grid(static_cast<unsigned>(p.tiles * (bm / (16 * MT))), a.slices, groups);
-  const int smem = kWarps * 16 * MT * 8 * NT * static_cast<int>(sizeof(float));
-  auto kern = p.large ? shrink_kernel<2, NT> : shrink_kernel<1, NT>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<grid, kThreads, smem, stream>>>(a, bm);
+cudaError_t launch_shrink_small(const Args& a, const Plan& p, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.tiles), a.slices, (a.R + kGroup - 1) / kGroup);
+  const int smem = kWarps * 16 * 8 * NT * static_cast<int>(sizeof(float));  // 32 KB at most
+  shrink_small_kernel<NT><<<grid, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int RN>
+cudaError_t launch_shrink_large(const Args& a, const Plan& p, cudaStream_t stream) {
+  CUtensorMap x, w;
+  if (!make_tensor_map_2d(&x, a.x, a.K, a.M, kStepK, kLargeRows, true, 2) ||
+      !make_tensor_map_2d(&w, a.a, a.K, static_cast<uint64_t>(a.adapters) * a.R, kStepK, RN, true, 2))
+    return cudaErrorInvalidValue;
+  auto kern = shrink_large_kernel<RN>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             ShrinkCfg<RN>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(static_cast<unsigned>(p.tiles), a.slices), kShrinkThreads, ShrinkCfg<RN>::kSmemBytes,
+         stream>>>(x, w, a);
+  return cudaGetLastError();
+}
+
+template <typename... Params>
+cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int smem, cudaStream_t stream,
+                          Params... params) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid, cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream, cfg.attrs = &attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, params...);
 }
 
 template <int KS>
 cudaError_t launch_expand(const Args& a, const Plan& p, cudaStream_t stream) {
-  const int cols = p.large ? 512 : 256;
-  const dim3 grid(static_cast<unsigned>(p.tiles), (a.N + cols - 1) / cols);
-  if (p.large)
-    expand_kernel<true, KS><<<grid, kThreads, 0, stream>>>(a, cols);
-  else
-    expand_kernel<false, KS><<<grid, kThreads, 0, stream>>>(a, cols);
-  return cudaGetLastError();
+  if (p.large) {
+    constexpr int smem = 2 * kLargeRows * (64 * KS + (KS % 2 == 0 ? 64 : 0));
+    auto kern = expand_large_kernel<KS>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(p.tiles), (a.N + 32 * kWarps - 1) / (32 * kWarps));
+    return launch_behind(kern, grid, smem, stream, a);
+  }
+  // a block's t costs as much as a few column groups: about five blocks per SM, up to eight groups
+  const int64_t groups = (a.N + 32 * kWarps - 1) / (32 * kWarps);
+  int64_t each = p.tiles * groups / (5 * kSms);
+  each = each < 1 ? 1 : each > 8 ? 8 : each;
+  const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>((groups + each - 1) / each));
+  return launch_behind(expand_small_kernel<KS>, grid, 0, stream, a,
+                       static_cast<int>(32 * kWarps * each));
 }
 
 inline cudaError_t launch(const Args& a, const Plan& p, cudaStream_t stream) {
   cudaError_t e;
-  if (a.R <= 8)
-    e = launch_shrink<1>(a, p, stream);
+  if (p.large)
+    switch ((a.R + 15) / 16) {
+      case 1: e = launch_shrink_large<16>(a, p, stream); break;
+      case 2: e = launch_shrink_large<32>(a, p, stream); break;
+      case 3: e = launch_shrink_large<48>(a, p, stream); break;
+      case 4: e = launch_shrink_large<64>(a, p, stream); break;
+      case 5: e = launch_shrink_large<80>(a, p, stream); break;
+      case 6: e = launch_shrink_large<96>(a, p, stream); break;
+      case 7: e = launch_shrink_large<112>(a, p, stream); break;
+      default: e = launch_shrink_large<128>(a, p, stream); break;
+    }
+  else if (a.R <= 8)
+    e = launch_shrink_small<1>(a, p, stream);
   else if (a.R <= 16)
-    e = launch_shrink<2>(a, p, stream);
+    e = launch_shrink_small<2>(a, p, stream);
   else if (a.R <= 32)
-    e = launch_shrink<4>(a, p, stream);
+    e = launch_shrink_small<4>(a, p, stream);
   else
-    e = launch_shrink<8>(a, p, stream);
+    e = launch_shrink_small<8>(a, p, stream);
   if (e != cudaSuccess) return e;
   switch ((a.R + 31) / 32) {
     case 1: return launch_expand<1>(a, p, stream);
