@@ -20,6 +20,7 @@ from .binding import (  # noqa: F401
     qs_qlinear, qs_qlinear_mixed, qs_quant_act, qs_selftest_timeout, qs_version, quant_act,
     QS_ATTN_CAUSAL, QS_BLOCK_K, QS_BLOCK_Q, QS_ROPE_INTERLEAVED, QS_ROPE_INVERSE, LoraBatch,
     block_attention, block_means, block_select, lora_add, qs_block_attention,
-    qs_block_attention_workspace_bytes, qs_block_means, qs_block_select, qs_lora_add,
+    qs_block_attention_workspace_bytes, qs_block_means, qs_block_select,
+    qs_block_select_workspace_bytes, qs_lora_add,
     qs_lora_workspace_bytes, qs_rope, rope, rope_frequencies,
 )

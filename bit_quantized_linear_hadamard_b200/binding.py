@@ -39,7 +39,8 @@ EXPORTS = ("qs_pack_weights", "qs_quant_act", "qs_qlinear", "qs_qlinear_mixed", 
            "qs_sd4_scale_tiles", "qs_sd4_linear_e4m3_tiles", "qs_sd4_quant_decomp",
            "qs_sd4_linear_decomp", "qs_gbs_reset", "qs_gbs_update", "qs_linear_gbs",
            "qs_selftest_timeout", "qs_device_error", "qs_status_str", "qs_version", "qs_rope",
-           "qs_lora_workspace_bytes", "qs_lora_add", "qs_block_means", "qs_block_select",
+           "qs_lora_workspace_bytes", "qs_lora_add", "qs_block_means",
+           "qs_block_select_workspace_bytes", "qs_block_select",
            "qs_block_attention_workspace_bytes", "qs_block_attention")
 QS_ROPE_INTERLEAVED, QS_ROPE_INVERSE = 1, 2
 QS_ATTN_CAUSAL = 1
@@ -123,8 +124,10 @@ def load() -> ctypes.CDLL:
     L.qs_lora_add.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, i64, i64, vp, vp, i64, vp, i64, vp,
                               vp]
     L.qs_block_means.argtypes = [vp, st, i64, i64, i64, i64, i32, vp, i64, vp, vp]
+    L.qs_block_select_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.qs_block_select_workspace_bytes.restype = i64
     L.qs_block_select.argtypes = [vp, st, i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64,
-                                  i64, u32, vp, vp]
+                                  i64, u32, vp, i64, vp, vp]
     L.qs_block_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
     L.qs_block_attention_workspace_bytes.restype = i64
     L.qs_block_attention.argtypes = [vp, st, vp, st, vp, st, i64, i64, i64, i64, i64, i64, i32, vp,
@@ -652,7 +655,11 @@ def qs_block_means(x, lens, first_block, means, stream=None):
                                  first_block, _p(means), _s(stream)), "qs_block_means")
 
 
-def qs_block_select(q, means, Lk, q_len, k_len, T, keep_first, keep_last, flags, blocks,
+def qs_block_select_workspace_bytes(B, Lq, Hq, D) -> int:
+    return int(load().qs_block_select_workspace_bytes(B, Lq, Hq, D))
+
+
+def qs_block_select(q, means, Lk, q_len, k_len, T, keep_first, keep_last, flags, workspace, blocks,
                     stream=None):
     """q: [B, Lq, Hq, D] view; means: float32 [B, Hkv, ceil(Lk / 64), D]; blocks: int32
     [B, Hq, ceil(Lq / 128), T]."""
@@ -665,13 +672,15 @@ def qs_block_select(q, means, Lk, q_len, k_len, T, keep_first, keep_last, flags,
     _shape(means, (B, Hkv, -(-Lk // QS_BLOCK_K), D), "means")
     _cuda(blocks, torch.int32, "blocks")
     _shape(blocks, (B, Hq, -(-Lq // QS_BLOCK_Q), T), "blocks")
+    _cuda(workspace, torch.uint8, "workspace")
     for t, name in ((q_len, "q_len"), (k_len, "k_len")):
         if t is not None:
             _cuda(t, torch.int32, name)
             _shape(t, (B,), name)
     _check(load().qs_block_select(_p(q), _Strides(*st[:3]), B, Lq, Hq, D, _DTYPES[q.dtype],
                                   _p(means), Lk, Hkv, _p(q_len), _p(k_len), T, keep_first, keep_last,
-                                  flags, _p(blocks), _s(stream)), "qs_block_select")
+                                  flags, _p(workspace), 0 if workspace is None else workspace.numel(),
+                                  _p(blocks), _s(stream)), "qs_block_select")
 
 
 def qs_block_attention_workspace_bytes(B, Lq, Hq, D, T) -> int:
@@ -947,17 +956,22 @@ def block_means(x, lens=None, first_block: int = 0, out=None, stream=None):
 
 
 def block_select(q, means, count: int, keys: int, first: int = 0, last: int = 0,
-                 causal: bool = False, q_len=None, k_len=None, out=None, stream=None):
+                 causal: bool = False, q_len=None, k_len=None, out=None, workspace=None,
+                 stream=None):
     """The ``count`` key blocks that each block of 128 queries of q [B, Lq, Hq, D] attends to, by
     the product of block means (``means`` from `block_means` of ``keys`` keys): int32
     [B, Hq, ceil(Lq / 128), count], ascending, -1 behind the last.  The ``first`` and ``last``
     visible blocks are always among them."""
     _view(q, "q")
-    B, Lq, Hq, _ = q.shape
+    B, Lq, Hq, D = q.shape
     if out is None:
         out = _empty((B, Hq, -(-Lq // QS_BLOCK_Q), count), torch.int32, q.device, stream)
+    if workspace is None:
+        need = qs_block_select_workspace_bytes(B, Lq, Hq, D)
+        if need > 0:
+            workspace = _empty((need,), torch.uint8, q.device, stream)
     qs_block_select(q, means, keys, q_len, k_len, count, first, last,
-                    QS_ATTN_CAUSAL if causal else 0, out, stream)
+                    QS_ATTN_CAUSAL if causal else 0, workspace, out, stream)
     return out
 
 

@@ -965,7 +965,7 @@ qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t
   QS_TRY(check_rows_k(M, K));
   if (N <= 0 || N % 16 != 0 || R < 8 || R % 8 != 0 || adapters <= 0 || requests <= 0)
     return QS_ERR_SHAPE;
-  if (N > QS_MAX_ROWS || R > qs::lora::kMaxRank || adapters > QS_MAX_ROWS / R ||
+  if (N > QS_MAX_ROWS || R > qs::lora::kMaxRank || adapters > QS_MAX_ROWS / (R > N ? R : N) ||
       requests > QS_MAX_ROWS - M)
     return QS_ERR_RANGE;
   const int64_t need = qs_lora_workspace_bytes(M, K, R, requests);
@@ -1008,7 +1008,7 @@ qs_status qs_block_means(const void* x, const qs_strides* x_strides, int64_t B, 
   qs::select::MeanArgs a{};
   a.x = static_cast<const uint16_t*>(x), a.st = select_strides(x_strides), a.len = len;
   a.means = means, a.L = L, a.B = static_cast<int>(B), a.H = static_cast<int>(H);
-  a.blocks = static_cast<int>(blocks), a.first = static_cast<int>(first_block);
+  a.blocks = static_cast<int>(blocks), a.first = static_cast<int>(first_block), a.size = QS_BLOCK_K;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = dtype == QS_F16;
   const cudaError_t e =
@@ -1017,11 +1017,18 @@ qs_status qs_block_means(const void* x, const qs_strides* x_strides, int64_t B, 
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 
+int64_t qs_block_select_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t D) {
+  if (B <= 0 || Lq <= 0 || Hq <= 0 || (D != 64 && D != 128)) return -1;
+  if (B > 65535 || Hq > 65535 || Lq > QS_MAX_LEN) return -1;
+  const int64_t means = B * Hq * ((Lq + QS_BLOCK_Q - 1) / QS_BLOCK_Q);
+  return means > qs::select::kOwnMeans ? means * D * 4 : 0;
+}
+
 qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B, int64_t Lq,
                           int64_t Hq, int64_t D, int dtype, const float* means, int64_t Lk,
                           int64_t Hkv, const int32_t* q_len, const int32_t* k_len, int64_t T,
-                          int64_t keep_first, int64_t keep_last, unsigned flags, int32_t* blocks,
-                          void* stream) {
+                          int64_t keep_first, int64_t keep_last, unsigned flags, void* workspace,
+                          int64_t workspace_bytes, int32_t* blocks, void* stream) {
   if (!q || !q_strides || !means || !blocks) return QS_ERR_NULL;
   QS_TRY(check_view(q, q_strides, B, Lq, Hq, D, dtype));
   if (Lk <= 0 || Hkv <= 0 || Hq % Hkv != 0 || T <= 0) return QS_ERR_SHAPE;
@@ -1030,6 +1037,13 @@ qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B,
       keep_last < 0 || (flags & ~QS_ATTN_CAUSAL))
     return QS_ERR_RANGE;
   if (!aligned16(means) || !aligned_to(blocks, 4)) return QS_ERR_ALIGN;
+  const int64_t need = qs_block_select_workspace_bytes(B, Lq, Hq, D);
+  if (need > 0) {
+    if (!workspace) return QS_ERR_NULL;
+    if (workspace_bytes < need || need / (D * 4) > QS_MAX_ROWS) return QS_ERR_RANGE;
+    if (!aligned16(workspace)) return QS_ERR_ALIGN;
+    QS_TRY(check_device_ptr(workspace));
+  }
   QS_TRY(check_ints(q_len));
   QS_TRY(check_ints(k_len));
   QS_TRY(check_device_ptr(means));
@@ -1043,11 +1057,12 @@ qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B,
   a.first = static_cast<int>(keep_first < nk ? keep_first : nk);
   a.last = static_cast<int>(keep_last < nk ? keep_last : nk);
   a.causal = (flags & QS_ATTN_CAUSAL) != 0;
+  float* ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = dtype == QS_F16;
   const cudaError_t e =
-      D == 64 ? (f16 ? qs::select::launch_select<64, true>(a, s) : qs::select::launch_select<64, false>(a, s))
-              : (f16 ? qs::select::launch_select<128, true>(a, s) : qs::select::launch_select<128, false>(a, s));
+      D == 64 ? (f16 ? qs::select::launch_select<64, true>(a, ws, s) : qs::select::launch_select<64, false>(a, ws, s))
+              : (f16 ? qs::select::launch_select<128, true>(a, ws, s) : qs::select::launch_select<128, false>(a, ws, s));
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 

@@ -21,9 +21,10 @@
 // consecutive k (16 bytes) of a 32-wide slice for two k16 steps, and the four threads of a row
 // read 64 consecutive bytes.
 //
-// Expand: the same fragments.  Large tiles: a warp holds its 32 columns of B in registers and goes
-// down the rows, t comes from shared memory, y from two row groups ahead; with B read for every row
-// group instead the L1's line accesses bound it (2.1 TB/s against 6 now).  Small tiles: a warp holds
+// Expand, large tiles: t lies in shared memory as tops and rest, y and B come and the result
+// leaves by TMA in chunks of 64 columns, the products are tcgen05 MMAs of 128 x 64 into tensor
+// memory.  Everything from global memory straight to mma.sync fragments was bound by the L1's line
+// accesses (2.1 TB/s; 3.3 with B held in registers).  Small tiles: fragments as above, a warp holds
 // t and goes along the columns.
 #pragma once
 
@@ -72,6 +73,7 @@ inline Plan plan(int64_t M, int64_t K, int64_t R, int64_t requests) {
   int64_t n = 2 * kSms / blocks;
   const int64_t most = p.large ? K / (16 * kStepK) : K / 512;
   if (n > most) n = most;
+  if (p.large && n > 4) n = 4;  // the second kernel reads every slice of t once per column range
   p.slices = static_cast<int>(n < 1 ? 1 : n);
   return p;
 }
@@ -312,6 +314,7 @@ __device__ __forceinline__ void load_t(const Args& a, int64_t row, int k, float 
   float t[8] = {};
   if (there && k < a.R) {
     const float* p = a.part + row * a.R + k;
+#pragma unroll 4
     for (int i = 0; i < a.slices; ++i, p += a.M * a.R) {
       const float4 u = *reinterpret_cast<const float4*>(p);
       const float4 v = *reinterpret_cast<const float4*>(p + 4);
@@ -373,76 +376,196 @@ __device__ __forceinline__ void load_b(const Args& a, int adapter, int n0, uint4
     }
 }
 
-// Large tiles.  KS: 32-wide steps of the rank.
-template <int KS>
-__global__ void __launch_bounds__(kThreads, KS <= 2 ? 2 : 1) expand_large_kernel(const Args a) {
-  // rows of t: tops and rest, padded so that two rows 8 threads read lie in different banks
-  constexpr int kStride = 64 * KS + (KS % 2 == 0 ? 64 : 0), kRowGroups = kLargeRows / 16;
-  extern __shared__ __align__(16) uint8_t t_smem[];
+// Large tiles.  KH: 64-wide parts of the rank.  Warp 0 loads, warp 1 issues, warps 2-5 (a row to a
+// thread) put t into shared memory, then add y to the products in the place of y; warp 6 sends the
+// chunks off and gives their stages back as soon as they have been read.
+template <int KH>
+struct ExpandCfg {
+  static constexpr int kCols = 64;                                   // of a chunk
+  static constexpr int kT = KH * kLargeRows * 128;                   // tops or rest
+  static constexpr int kY = kLargeRows * 128, kB = KH * kCols * 128, kStage = kY + kB;
+  static constexpr int kStages = KH == 1 ? 3 : 4;                    // two CTAs per SM, or one
+  static constexpr int kOffStage = 2 * kT, kOffBar = kOffStage + kStages * kStage;
+  static constexpr int kFull = 0, kEmpty = kStages, kDFull = 2 * kStages, kDFree = kDFull + 2;
+  static constexpr int kSum = kDFree + 2, kTFull = kSum + kStages, kDrain = kTFull + 1;
+  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kSmemBytes = kOffBar + 8 * kNumBars + 16 + 1024;
+  static_assert(kSmemBytes <= (KH == 1 ? 113 : 227) * 1024, "shared memory per CTA");
+};
+constexpr int kExpandThreads = 32 * 7;
+
+template <int KH>
+__global__ void __launch_bounds__(kExpandThreads)
+    expand_large_kernel(const __grid_constant__ CUtensorMap tmY,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmO, const Args a, int chunks_each) {
+  using C = ExpandCfg<KH>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  uint8_t* sp = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + C::kOffBar + 8 * C::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const auto bar = [&](int i) { return sbase + C::kOffBar + 8u * i; };
   const Tile tile = find_tile(a, blockIdx.x, kLargeRows);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const bool turned = tile.adapter >= 0;
-  if (tile.rows <= 0 || (!turned && a.out == a.y)) {
+  const int chunks = (a.N + C::kCols - 1) / C::kCols;
+  const int first = blockIdx.y * chunks_each, n = min(chunks_each, chunks - first);
+  if (tile.rows <= 0 || n <= 0 || !turned) {
+    if (tile.rows > 0 && n > 0 && a.out != a.y) {  // no adapter: y as it is
+      const int pieces = min(n * C::kCols, a.N - first * C::kCols) / 8;
+      for (int64_t i = threadIdx.x; i < static_cast<int64_t>(tile.rows) * pieces; i += kExpandThreads) {
+        const int64_t at = (tile.row0 + i / pieces) * a.N + first * C::kCols + 8 * (i % pieces);
+        *reinterpret_cast<uint4*>(a.out + at) = *reinterpret_cast<const uint4*>(a.y + at);
+      }
+    }
     wait_for_shrink();
     return;
   }
-  const int n0 = 32 * (blockIdx.y * kWarps + warp);
-  const bool in = n0 + 8 * c < a.N;  // N is a multiple of 16, a warp's columns are 32
-  uint4 w[KS][4];
-  if (turned) load_b<KS>(a, tile.adapter, n0, w);
-  const int64_t at = static_cast<int64_t>(tile.row0 + g) * a.N + n0 + 8 * c;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const auto load_y = [&](int rg, int h) {
-    const int r = 16 * rg + 8 * h;
-    return in && r + g < tile.rows
-               ? *reinterpret_cast<const uint4*>(a.y + at + static_cast<int64_t>(r) * a.N)
-               : zero;
-  };
-  uint4 y[3][2];  // of this row group and the next two
-#pragma unroll
-  for (int d = 0; d < 2; ++d)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) y[d][h] = load_y(d, h);
-  wait_for_shrink();
-  if (turned) {
-    const float scale = a.scale ? a.scale[tile.adapter] : 1.f;
-    for (int i = threadIdx.x; i < kLargeRows * 4 * KS; i += kThreads) {
-      const int r = i / (4 * KS), k = 8 * (i % (4 * KS));
-      uint4 hi, lo;
-      load_t(a, tile.row0 + r, k, scale, r < tile.rows, hi, lo);
-      *reinterpret_cast<uint4*>(t_smem + r * kStride + 2 * k) = hi;
-      *reinterpret_cast<uint4*>(t_smem + (kLargeRows + r) * kStride + 2 * k) = lo;
-    }
-    __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNumBars; ++i)
+      mbar_init(bar(i), i >= C::kDFree && i <= C::kTFull ? 4 : 1);  // the four row warps'
+    *abort_flag = 0;
+    fence_mbar_init();
   }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 2 * C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // After a wait that gave up, a thread waits for nothing more and runs its loops out.
+  bool ok = true;
+  const auto wait = [&](int i, uint32_t parity, unsigned err) {
+    if (ok) ok = mbar_wait_bounded(bar(i), parity, abort_flag, err);
+  };
+
+  if (warp == 0 && lane == 0) {
+    int i = 0;
+    for (; i < n; ++i) {
+      const int s = i % C::kStages;
+      wait(C::kEmpty + s, ((i / C::kStages) & 1) ^ 1, kErrWaitProducer);
+      if (!ok) break;
+      const uint32_t dst = sbase + C::kOffStage + s * C::kStage;
+      const int c0 = (first + i) * C::kCols;
+      mbar_arrive_expect_tx(bar(C::kFull + s), C::kStage);
+      tma_load_2d(dst, &tmY, c0, tile.row0, bar(C::kFull + s));
+      for (int h = 0; h < KH; ++h)
+        tma_load_2d(dst + C::kY + h * C::kCols * 128, &tmB, 64 * h, tile.adapter * a.N + c0,
+                    bar(C::kFull + s));
+    }
+    // no copy into this CTA's memory may outlive it
+    for (int k = i > C::kStages ? i - C::kStages : 0; k < i; ++k)
+      mbar_wait_limit(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitTimeoutNs,
+                      kErrWaitTma);
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |  // binary32 D, bf16 A and B
+                               (static_cast<uint32_t>(C::kCols >> 3) << 17) |
+                               (static_cast<uint32_t>(kLargeRows >> 4) << 24);
+    const int steps = (a.R + 15) / 16;
+    wait(C::kTFull, 0, kErrWaitEpilogue);
+    for (int i = 0; i < n && ok; ++i) {
+      const int s = i % C::kStages, buf = i & 1;
+      wait(C::kFull + s, (i / C::kStages) & 1, kErrWaitTma);
+      wait(C::kDFree + buf, ((i >> 1) & 1) ^ 1, kErrWaitEpilogue);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t b = sbase + C::kOffStage + s * C::kStage + C::kY;
+      for (int part = 0; part < 2; ++part)  // tops, rest
+        for (int k = 0; k < steps; ++k)
+          mma_bf16_ss(tmem + C::kCols * buf,
+                      smem_desc_sw128(sbase + part * C::kT + (k / 4) * kLargeRows * 128 + (k % 4) * 32),
+                      smem_desc_sw128(b + (k / 4) * C::kCols * 128 + (k % 4) * 32), idesc,
+                      part != 0 || k != 0);
+      mma_commit(bar(C::kDFull + buf));
+    }
+    mma_commit(bar(C::kDrain));
+    mbar_wait_limit(bar(C::kDrain), 0, kWaitTimeoutNs, kErrWaitMma);
+  } else if (warp >= 2 && warp < 6) {
+    const int thread = threadIdx.x - 64;
+    wait_for_shrink();
+    {
+      const float scale = a.scale ? a.scale[tile.adapter] : 1.f;
+#pragma unroll 4
+      for (int i = thread; i < kLargeRows * 8 * KH; i += 128) {
+        const int r = i / (8 * KH), p = i % (8 * KH);  // row, piece of 8 ranks
+        uint4 hi, lo;
+        load_t(a, tile.row0 + r, 8 * p, scale, r < tile.rows, hi, lo);
+        uint8_t* at = sp + (p / 8) * kLargeRows * 128 + r * 128 + 16 * ((p & 7) ^ (r & 7));
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + C::kT) = lo;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kTFull));
+    }
+    const int quarter = warp & 3, r = 32 * quarter + lane;  // the lanes of tensor memory it may read
+    const bool whole = tile.rows == kLargeRows;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % C::kStages, buf = i & 1, c0 = (first + i) * C::kCols;
+      wait(C::kFull + s, (i / C::kStages) & 1, kErrWaitTma);
+      wait(C::kDFull + buf, (i >> 1) & 1, kErrWaitMma);
+      __syncwarp();
+      tc_fence_after();
+      uint8_t* y = sp + C::kOffStage + s * C::kStage + r * 128;
+      uint16_t* out = a.out + (static_cast<int64_t>(tile.row0) + r) * a.N + c0;
 #pragma unroll
-  for (int rg = 0; rg < kRowGroups; ++rg) {
-    if (16 * rg >= tile.rows) break;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kCols * buf + 32 * h, d);
+        tmem_wait_ld();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) y[(rg + 2) % 3][h] = rg + 2 < kRowGroups ? load_y(rg + 2, h) : zero;
-    float acc[4][4] = {};
-    if (turned) {
+        for (int p = 0; p < 4; ++p) {
+          uint4* at = reinterpret_cast<uint4*>(y + 16 * ((4 * h + p) ^ (r & 7)));
+          const uint4 v = *at;
+          const uint32_t yw[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        uint4 hi[2], lo[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* p = t_smem + (16 * rg + 8 * h + g) * kStride + 64 * s + 16 * c;
-          hi[h] = *reinterpret_cast<const uint4*>(p);
-          lo[h] = *reinterpret_cast<const uint4*>(p + kLargeRows * kStride);
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 e = __floats2bfloat162_rn(
+                __uint_as_float(yw[j] << 16) + __uint_as_float(d[8 * p + 2 * j]),
+                __uint_as_float(yw[j] & 0xFFFF0000u) + __uint_as_float(d[8 * p + 2 * j + 1]));
+            o[j] = *reinterpret_cast<const uint32_t*>(&e);
+          }
+          if (whole)
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
+          else if (r < tile.rows && ok && c0 + 32 * h + 8 * p < a.N)
+            *reinterpret_cast<uint4*>(out + 32 * h + 8 * p) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_t(acc[j], hi, lo, w[s][j]);
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::kDFree + buf));
+        mbar_arrive(bar(C::kSum + s));
       }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 16 * rg + 8 * h;
-      if (!in || r + g >= tile.rows) continue;
-      *reinterpret_cast<uint4*>(a.out + at + static_cast<int64_t>(r) * a.N) =
-          turned ? add_y(y[rg % 3][h], acc, h) : y[rg % 3][h];
+  } else if (warp == 6 && lane == 0) {
+    for (int i = 0; i < n && ok; ++i) {
+      const int s = i % C::kStages;
+      wait(C::kSum + s, (i / C::kStages) & 1, kErrWaitEpilogue);
+      if (!ok) break;
+      if (tile.rows == kLargeRows) {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+            "cp.async.bulk.commit_group;\n\t"
+            "cp.async.bulk.wait_group.read 0;" ::"l"(reinterpret_cast<uint64_t>(&tmO)),
+            "r"((first + i) * C::kCols), "r"(tile.row0), "r"(sbase + C::kOffStage + s * C::kStage)
+            : "memory");
+      }
+      mbar_arrive(bar(C::kEmpty + s));
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 2 * C::kCols);
 }
 
 // Small tiles: the warp's t in registers, 32 columns at a time.
@@ -513,34 +636,49 @@ cudaError_t launch_shrink_large(const Args& a, const Plan& p, cudaStream_t strea
 }
 
 template <typename... Params>
-cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int smem, cudaStream_t stream,
-                          Params... params) {
+cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, int smem,
+                          cudaStream_t stream, Params... params) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid, cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
   cfg.stream = stream, cfg.attrs = &attr, cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, params...);
 }
 
+template <int KH>
+cudaError_t launch_expand_large(const Args& a, const Plan& p, cudaStream_t stream) {
+  using C = ExpandCfg<KH>;
+  CUtensorMap y, w, o;
+  if (!make_tensor_map_2d(&y, a.y, a.N, a.M, C::kCols, kLargeRows, true, 2) ||
+      !make_tensor_map_2d(&w, a.b, a.R, static_cast<uint64_t>(a.adapters) * a.N, 64, C::kCols, true, 2) ||
+      !make_tensor_map_2d(&o, a.out, a.N, a.M, C::kCols, kLargeRows, true, 2))
+    return cudaErrorInvalidValue;
+  auto kern = expand_large_kernel<KH>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  // one round of blocks, or more where a block would have over 27 chunks; a block's t should not
+  // be more to read than its y
+  const int64_t chunks = (a.N + C::kCols - 1) / C::kCols;
+  const int64_t t_chunks = (static_cast<int64_t>(a.R) * a.slices * kLargeRows * 4 + C::kY - 1) / C::kY;
+  int64_t each = (p.tiles * chunks + 2 * kSms - 1) / (2 * kSms);
+  each = each > 27 ? 27 : each;
+  each = each < t_chunks ? t_chunks : each;
+  const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>((chunks + each - 1) / each));
+  return launch_behind(kern, grid, kExpandThreads, C::kSmemBytes, stream, y, w, o, a,
+                       static_cast<int>(each));
+}
+
 template <int KS>
-cudaError_t launch_expand(const Args& a, const Plan& p, cudaStream_t stream) {
-  if (p.large) {
-    constexpr int smem = 2 * kLargeRows * (64 * KS + (KS % 2 == 0 ? 64 : 0));
-    auto kern = expand_large_kernel<KS>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(p.tiles), (a.N + 32 * kWarps - 1) / (32 * kWarps));
-    return launch_behind(kern, grid, smem, stream, a);
-  }
+cudaError_t launch_expand_small(const Args& a, const Plan& p, cudaStream_t stream) {
   // a block's t costs as much as a few column groups: about five blocks per SM, up to eight groups
   const int64_t groups = (a.N + 32 * kWarps - 1) / (32 * kWarps);
   int64_t each = p.tiles * groups / (5 * kSms);
   each = each < 1 ? 1 : each > 8 ? 8 : each;
   const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>((groups + each - 1) / each));
-  return launch_behind(expand_small_kernel<KS>, grid, 0, stream, a,
+  return launch_behind(expand_small_kernel<KS>, grid, kThreads, 0, stream, a,
                        static_cast<int>(32 * kWarps * each));
 }
 
@@ -566,11 +704,13 @@ inline cudaError_t launch(const Args& a, const Plan& p, cudaStream_t stream) {
   else
     e = launch_shrink_small<8>(a, p, stream);
   if (e != cudaSuccess) return e;
+  if (p.large)
+    return a.R <= 64 ? launch_expand_large<1>(a, p, stream) : launch_expand_large<2>(a, p, stream);
   switch ((a.R + 31) / 32) {
-    case 1: return launch_expand<1>(a, p, stream);
-    case 2: return launch_expand<2>(a, p, stream);
-    case 3: return launch_expand<3>(a, p, stream);
-    default: return launch_expand<4>(a, p, stream);
+    case 1: return launch_expand_small<1>(a, p, stream);
+    case 2: return launch_expand_small<2>(a, p, stream);
+    case 3: return launch_expand_small<3>(a, p, stream);
+    default: return launch_expand_small<4>(a, p, stream);
   }
 }
 

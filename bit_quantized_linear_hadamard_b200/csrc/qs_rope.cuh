@@ -117,61 +117,65 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
   __syncthreads();
 
   constexpr int W = INTER && V == 1 ? 2 : V;  // elements an interleaved item covers
+  constexpr bool kPartner = !INTER || V == 1;  // a pair's second element comes with another access
+  constexpr int kUnits = 4;                    // (row, head) units in flight per thread
   const int turn_items = INTER ? 2 * a.pairs / W : a.pairs / V;
   const int tail_items = a.copy_tail ? (a.dim - 2 * a.pairs) / V : 0;
   const int items = turn_items + tail_items;
   const int h0 = blockIdx.y * a.heads_per_block;
-  const int nheads = min(a.heads_per_block, a.heads - h0);
-  // thread -> (item, first head); more items than threads: several passes over the items
+  const unsigned nheads = min(a.heads_per_block, a.heads - h0);
+  // thread -> (item, first unit); more items than threads: several passes over the items
   const int lanes = items < kThreads ? kThreads / items : 1;
   const int item_step = items < kThreads ? items : kThreads;
   const int lane = threadIdx.x / item_step;
   if (lane >= lanes) return;
   using P = Vec<T, V>;
+  const int other = INTER ? 1 : a.pairs;  // distance of a pair's second element
+  const unsigned units = nrows * nheads;
   for (int it = threadIdx.x - lane * item_step; it < items; it += item_step) {
     const bool turn = it < turn_items;
     const int e0 = turn ? it * W : 2 * a.pairs + (it - turn_items) * V;
-    for (int r = 0; r < nrows; ++r) {
-      const T* xr = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + h0 * a.x_head + e0;
-      T* yr = static_cast<T*>(a.y) + (row0 + r) * a.y_row + h0 * a.y_head + e0;
-      const float2* cs = table + r * a.pairs + (INTER ? e0 / 2 : e0);
-      if (!turn) {
-        for (int h = lane; h < nheads; h += lanes)
-          *reinterpret_cast<P*>(yr + h * a.y_head) =
-              *reinterpret_cast<const P*>(xr + h * a.x_head);
-      } else if (INTER && V > 1) {
-        float2 f[V / 2 > 0 ? V / 2 : 1];
+    const T* x = static_cast<const T*>(a.x) + row0 * a.x_row + h0 * a.x_head + e0;
+    T* y = static_cast<T*>(a.y) + row0 * a.y_row + h0 * a.y_head + e0;
+    for (unsigned u0 = lane; u0 < units; u0 += kUnits * lanes) {
+      // all loads before the first store: x and y may be one, so the compiler keeps their order
+      P u[kUnits], w[kUnits];
+      unsigned r[kUnits], h[kUnits];
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) f[k] = cs[k];
-#pragma unroll 4
-        for (int h = lane; h < nheads; h += lanes) {
-          P u = *reinterpret_cast<const P*>(xr + h * a.x_head);
+      for (int k = 0; k < kUnits; ++k) {
+        const unsigned i = u0 + k * lanes;
+        if (i >= units) continue;
+        r[k] = i / nheads, h[k] = i - r[k] * nheads;
+        const T* p = x + r[k] * a.x_row + h[k] * a.x_head;
+        u[k] = *reinterpret_cast<const P*>(p);
+        if (kPartner && turn) w[k] = *reinterpret_cast<const P*>(p + other);
+      }
 #pragma unroll
-          for (int k = 0; k < V / 2; ++k) {
-            const float p = to_f32(u.v[2 * k]), q = to_f32(u.v[2 * k + 1]);
-            u.v[2 * k] = from_f32<T>(p * f[k].x - q * f[k].y);
-            u.v[2 * k + 1] = from_f32<T>(p * f[k].y + q * f[k].x);
+      for (int k = 0; k < kUnits; ++k) {
+        if (u0 + k * lanes >= units) continue;
+        T* p = y + r[k] * a.y_row + h[k] * a.y_head;
+        if (turn) {
+          const float2* cs = table + r[k] * a.pairs + (INTER ? e0 / 2 : e0);
+          if (kPartner) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const float2 f = cs[j];
+              const float m = to_f32(u[k].v[j]), n = to_f32(w[k].v[j]);
+              u[k].v[j] = from_f32<T>(m * f.x - n * f.y);
+              w[k].v[j] = from_f32<T>(m * f.y + n * f.x);
+            }
+            *reinterpret_cast<P*>(p + other) = w[k];
+          } else {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+              const float2 f = cs[j];
+              const float m = to_f32(u[k].v[2 * j]), n = to_f32(u[k].v[2 * j + 1]);
+              u[k].v[2 * j] = from_f32<T>(m * f.x - n * f.y);
+              u[k].v[2 * j + 1] = from_f32<T>(m * f.y + n * f.x);
+            }
           }
-          *reinterpret_cast<P*>(yr + h * a.y_head) = u;
         }
-      } else {
-        const int other = INTER ? 1 : a.pairs;  // distance of a pair's second element
-        float2 f[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) f[k] = cs[k];
-#pragma unroll 4
-        for (int h = lane; h < nheads; h += lanes) {
-          P u = *reinterpret_cast<const P*>(xr + h * a.x_head);
-          P w = *reinterpret_cast<const P*>(xr + h * a.x_head + other);
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float p = to_f32(u.v[k]), q = to_f32(w.v[k]);
-            u.v[k] = from_f32<T>(p * f[k].x - q * f[k].y);
-            w.v[k] = from_f32<T>(p * f[k].y + q * f[k].x);
-          }
-          *reinterpret_cast<P*>(yr + h * a.y_head) = u;
-          *reinterpret_cast<P*>(yr + h * a.y_head + other) = w;
-        }
+        *reinterpret_cast<P*>(p) = u[k];
       }
     }
   }

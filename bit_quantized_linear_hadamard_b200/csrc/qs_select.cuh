@@ -11,7 +11,10 @@
 // ones do not.  Sums of bf16 or fp16 values are exact in binary64 for all practical ranges, the
 // products of two binary32 means are exact, and 128 of them are summed.
 //
-// Bound by HBM: queries and keys are read once; the scores stay in shared memory.
+// Bound by HBM: queries and keys are read once; the scores stay in shared memory.  The query means
+// have a kernel of their own (62 us for the 335 MB of a video's queries; formed by the blocks that
+// go on to the scores, whose registers leave room for few warps, 150), but for few of them: there
+// a launch costs more.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,6 +45,7 @@ struct MeanArgs {
   float* means;        // [B, H, blocks, D]
   int64_t L;
   int B, H, blocks, first;
+  int size;            // rows of a block
 };
 
 struct SelectArgs {
@@ -55,6 +59,7 @@ struct SelectArgs {
   int first, last;     // blocks always kept at the two ends of the visible ones
   int causal;
   int rows;            // query blocks per CTA, <= kRows
+  const float* q_means; // [B, Hq, nq, D], or NULL: the CTAs form them
 };
 
 template <bool F16>
@@ -116,8 +121,8 @@ __global__ void __launch_bounds__(kThreads) means_kernel(const MeanArgs a) {
   if (i >= static_cast<int64_t>(a.B) * count * a.H) return;
   const int h = static_cast<int>(i % a.H), j = static_cast<int>(i / a.H % count) + a.first;
   const int b = static_cast<int>(i / a.H / count);
-  const int64_t len = checked_len(a.len, b, a.L), row0 = static_cast<int64_t>(j) * QS_BLOCK_K;
-  const int rows = static_cast<int>(max(int64_t{0}, min(len - row0, int64_t{QS_BLOCK_K})));
+  const int64_t len = checked_len(a.len, b, a.L), row0 = static_cast<int64_t>(j) * a.size;
+  const int rows = static_cast<int>(max(int64_t{0}, min(len - row0, static_cast<int64_t>(a.size))));
   double sum[8];
   warp_row_sum<D, F16>(a.x + b * a.st.batch + h * a.st.head + row0 * a.st.row, a.st.row, rows, sum);
   const int lane = threadIdx.x & 31;
@@ -144,54 +149,65 @@ __device__ __forceinline__ unsigned long long score_key(double s) {
   return v < 0 ? ~u : u | 0x8000000000000000ull;
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
-  extern __shared__ unsigned long long keys[];  // [rows][nk], behind it the query means
-  float* qm = reinterpret_cast<float*>(keys + static_cast<int64_t>(a.rows) * a.nk);  // [8][D]
+// OWN: the query means are formed here.
+template <int D, bool F16, bool OWN>
+__global__ void __launch_bounds__(kThreads, OWN ? 2 : 3) select_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) double qm[];  // query means [8][D], behind them the keys [rows][nk]
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(qm + kRows * D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y, b = blockIdx.z;
   const int i0 = blockIdx.x * a.rows;
   const int64_t ql = checked_len(a.q_len, b, a.Lq), kl = checked_len(a.k_len, b, a.Lk);
 
-  // query means: a warp forms one row's
-  for (int r = warp; r < kRows; r += kWarps) {
-    const int64_t row0 = static_cast<int64_t>(i0 + r) * QS_BLOCK_Q;
-    const int rows =
-        r < a.rows ? static_cast<int>(max(int64_t{0}, min(ql - row0, int64_t{QS_BLOCK_Q}))) : 0;
-    double sum[8];
-    warp_row_sum<D, F16>(a.q + b * a.st.batch + h * a.st.head + row0 * a.st.row, a.st.row, rows,
-                         sum);
-    const double n = rows > 0 ? rows : 1;
-    if (lane < D / 8)
+  // query means, rounded to binary32 as the keys' are
+  if (OWN) {
+    for (int r = warp; r < kRows; r += kWarps) {
+      const int64_t row0 = static_cast<int64_t>(i0 + r) * QS_BLOCK_Q;
+      const int rows =
+          r < a.rows ? static_cast<int>(max(int64_t{0}, min(ql - row0, int64_t{QS_BLOCK_Q}))) : 0;
+      double sum[8];
+      warp_row_sum<D, F16>(a.q + b * a.st.batch + h * a.st.head + row0 * a.st.row, a.st.row, rows,
+                           sum);
+      const double n = rows > 0 ? rows : 1;
+      if (lane < D / 8)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qm[r * D + lane * 8 + e] = static_cast<float>(sum[e] / n);
+        for (int e = 0; e < 8; ++e) qm[r * D + lane * 8 + e] = static_cast<float>(sum[e] / n);
+    }
+  } else {
+    const float* src = a.q_means + ((static_cast<int64_t>(b) * a.Hq + h) * a.nq + i0) * D;
+    const int have = min(a.rows, a.nq - i0) * D;
+    for (int i = threadIdx.x; i < kRows * D; i += kThreads) qm[i] = i < have ? src[i] : 0.f;
   }
   __syncthreads();
 
   // scores: a warp takes 8 key blocks; a thread's four columns of a 16-wide slice serve as k of
-  // four m8n8k4 steps (the order of k is free as long as both operands share it)
+  // four m8n8k4 steps (the order of k is free as long as both operands share it), each with sums
+  // of its own: 32 steps on one would wait for each other
   const int g = lane >> 2, c = lane & 3;
   const float* km = a.means +
                     (static_cast<int64_t>(b) * a.Hkv + h / (a.Hq / a.Hkv)) * a.nk * D;
-  double aq[D / 4];
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) aq[4 * s + e] = qm[g * D + 16 * s + 4 * c + e];
+  const double2* aq = reinterpret_cast<const double2*>(qm + g * D + 4 * c);
   for (int j0 = 8 * warp; j0 < a.nk; j0 += 8 * kWarps) {
     const int j = min(j0 + g, a.nk - 1);
-    double d[2] = {0.0, 0.0};
-    float4 f[D / 16];
+    double d4[4][2] = {};
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      f[s] = __ldg(reinterpret_cast<const float4*>(km + static_cast<int64_t>(j) * D + 16 * s + 4 * c));
+    for (int s0 = 0; s0 < D / 16; s0 += 4) {
+      float4 f[4];
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      mma_f64(d, aq[4 * s], f[s].x);
-      mma_f64(d, aq[4 * s + 1], f[s].y);
-      mma_f64(d, aq[4 * s + 2], f[s].z);
-      mma_f64(d, aq[4 * s + 3], f[s].w);
+      for (int s = 0; s < 4; ++s)
+        f[s] = __ldg(reinterpret_cast<const float4*>(km + static_cast<int64_t>(j) * D +
+                                                     16 * (s0 + s) + 4 * c));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const double2 q01 = aq[8 * (s0 + s)], q23 = aq[8 * (s0 + s) + 1];
+        mma_f64(d4[0], q01.x, f[s].x);
+        mma_f64(d4[1], q01.y, f[s].y);
+        mma_f64(d4[2], q23.x, f[s].z);
+        mma_f64(d4[3], q23.y, f[s].w);
+      }
     }
+    const double d[2] = {(d4[0][0] + d4[1][0]) + (d4[2][0] + d4[3][0]),
+                         (d4[0][1] + d4[1][1]) + (d4[2][1] + d4[3][1])};
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (g < a.rows && j0 + 2 * c + e < a.nk)
@@ -257,14 +273,24 @@ cudaError_t launch_means(const MeanArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Query means formed on the way: up to this many query blocks in all.
+constexpr int64_t kOwnMeans = 1024;
+
 template <int D, bool F16>
-cudaError_t launch_select(SelectArgs a, cudaStream_t stream) {
+cudaError_t launch_select(SelectArgs a, float* workspace, cudaStream_t stream) {
   a.rows = kRows;
   const auto smem = [&] {
-    return static_cast<int64_t>(a.rows) * a.nk * 8 + kRows * D * static_cast<int>(sizeof(float));
+    return static_cast<int64_t>(a.rows) * a.nk * 8 + kRows * D * static_cast<int>(sizeof(double));
   };
   while (a.rows > 1 && (smem() > kMaxSmem || a.rows / 2 >= a.nq)) a.rows /= 2;
-  auto kern = select_kernel<D, F16>;
+  const bool own = workspace == nullptr;
+  if (!own) {
+    MeanArgs m{a.q, a.st, a.q_len, workspace, a.Lq, a.B, a.Hq, a.nq, 0, QS_BLOCK_Q};
+    const cudaError_t e = launch_means<D, F16>(m, stream);
+    if (e != cudaSuccess) return e;
+    a.q_means = workspace;
+  }
+  auto kern = own ? select_kernel<D, F16, true> : select_kernel<D, F16, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kMaxSmem);
   if (e != cudaSuccess) return e;

@@ -647,15 +647,20 @@ QS_API qs_status qs_block_means(const void* x, const qs_strides* x_strides, int6
  *   means   [B, Hkv, ceil(Lk / QS_BLOCK_K), D] float (qs_block_means), 16-byte
  *           aligned; Hq % Hkv == 0, query head h reads key head h / (Hq / Hkv);
  *           at most QS_MAX_SELECT_BLOCKS blocks
+ *   workspace  qs_block_select_workspace_bytes(B, Lq, Hq, D) bytes of device
+ *           scratch, 16-byte aligned (0: none is needed and it may be NULL; -1
+ *           for rejected arguments)
  *   blocks  [B, Hq, ceil(Lq / QS_BLOCK_Q), T] int32, written: ascending, -1
  *           behind the last (all -1 for a query block behind q_len)
  */
+QS_API int64_t qs_block_select_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t D);
 QS_API qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B,
                                  int64_t Lq, int64_t Hq, int64_t D, int dtype,
                                  const float* means, int64_t Lk, int64_t Hkv,
                                  const int32_t* q_len, const int32_t* k_len, int64_t T,
                                  int64_t keep_first, int64_t keep_last, unsigned flags,
-                                 int32_t* blocks, void* stream);
+                                 void* workspace, int64_t workspace_bytes, int32_t* blocks,
+                                 void* stream);
 
 /*
  * qs_block_attention — softmax(scale q k^T) v over the keys of the listed
