@@ -97,12 +97,37 @@ struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
 
+// A thread's way through the (row, head) units of a block: from unit `lane` in steps of `lanes`,
+// with the offsets of x and y carried along (a division and two 64-bit products per unit made the
+// kernel bound by its instructions: 333 us for 1.34 GB).
+struct Walk {
+  int64_t x, y;          // offsets of this unit
+  int64_t dx, dy;        // of a step
+  int64_t wx, wy;        // correction where a step passes the last head
+  unsigned row, head, d_row, d_head, heads;
+  __device__ Walk(const Args& a, unsigned lane, unsigned lanes, unsigned nheads) : heads(nheads) {
+    row = lane / nheads, head = lane - row * nheads;
+    d_row = lanes / nheads, d_head = lanes - d_row * nheads;
+    x = row * a.x_row + head * a.x_head, y = row * a.y_row + head * a.y_head;
+    dx = d_row * a.x_row + d_head * a.x_head, dy = d_row * a.y_row + d_head * a.y_head;
+    wx = a.x_row - nheads * a.x_head, wy = a.y_row - nheads * a.y_head;
+  }
+  __device__ __forceinline__ void step() {
+    row += d_row, head += d_head, x += dx, y += dy;
+    if (head >= heads) head -= heads, ++row, x += wx, y += wy;
+  }
+};
+
 // V elements per access; with V == 1 any stride and any alignment of the elements does.
 // INTER: an item is V elements of a head (V/2 pairs; 2 elements for V == 1).  Halves: an item is
-// V elements of the first half and their partners.  Items behind the pairs copy V elements.
+// V elements of the first half and their partners.  The elements behind the pairs are copied in a
+// second pass, V at a time.
+// One unit per thread and many blocks: two or four units with all their loads first were slower
+// (1.34 GB, interleaved: 254 us against 302 and 376), the memory being read and written in more
+// places at once.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
-  extern __shared__ float2 table[];  // [rows_per_block][pairs]
+__global__ void __launch_bounds__(kThreads, !INTER || V == 1 ? 4 : 8) rope_kernel(const Args a) {
+  extern __shared__ __align__(16) float2 table[];  // [rows_per_block][pairs]
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_block;
   const int nrows = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - row0));
   for (int i = threadIdx.x; i < nrows * a.pairs; i += kThreads) {
@@ -116,69 +141,56 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args a) {
   }
   __syncthreads();
 
-  constexpr int W = INTER && V == 1 ? 2 : V;  // elements an interleaved item covers
+  constexpr int W = INTER && V == 1 ? 2 : V;   // elements an interleaved item covers
   constexpr bool kPartner = !INTER || V == 1;  // a pair's second element comes with another access
-  constexpr int kUnits = 4;                    // (row, head) units in flight per thread
-  const int turn_items = INTER ? 2 * a.pairs / W : a.pairs / V;
-  const int tail_items = a.copy_tail ? (a.dim - 2 * a.pairs) / V : 0;
-  const int items = turn_items + tail_items;
   const int h0 = blockIdx.y * a.heads_per_block;
   const unsigned nheads = min(a.heads_per_block, a.heads - h0);
-  // thread -> (item, first unit); more items than threads: several passes over the items
-  const int lanes = items < kThreads ? kThreads / items : 1;
-  const int item_step = items < kThreads ? items : kThreads;
-  const int lane = threadIdx.x / item_step;
-  if (lane >= lanes) return;
-  using P = Vec<T, V>;
-  const int other = INTER ? 1 : a.pairs;  // distance of a pair's second element
   const unsigned units = nrows * nheads;
-  for (int it = threadIdx.x - lane * item_step; it < items; it += item_step) {
-    const bool turn = it < turn_items;
-    const int e0 = turn ? it * W : 2 * a.pairs + (it - turn_items) * V;
-    const T* x = static_cast<const T*>(a.x) + row0 * a.x_row + h0 * a.x_head + e0;
-    T* y = static_cast<T*>(a.y) + row0 * a.y_row + h0 * a.y_head + e0;
-    for (unsigned u0 = lane; u0 < units; u0 += kUnits * lanes) {
-      // all loads before the first store: x and y may be one, so the compiler keeps their order
-      P u[kUnits], w[kUnits];
-      unsigned r[kUnits], h[kUnits];
+  const T* x0 = static_cast<const T*>(a.x) + row0 * a.x_row + h0 * a.x_head;
+  T* y0 = static_cast<T*>(a.y) + row0 * a.y_row + h0 * a.y_head;
+  using P = Vec<T, V>;
+  // thread -> (item, first unit); more items than threads: several passes over the items
+  const auto each = [&](int items, auto&& body) {
+    const int step = items < kThreads ? items : kThreads;
+    const unsigned lanes = kThreads / step, lane = threadIdx.x / step;
+    if (lane >= lanes) return;
+    for (int it = threadIdx.x - lane * step; it < items; it += step) {
+      Walk at(a, lane, lanes, nheads);
+      for (unsigned u = lane; u < units; u += lanes, at.step()) body(it, at);
+    }
+  };
+
+  each(INTER ? 2 * a.pairs / W : a.pairs / V, [&](int it, const Walk& at) {
+    const T* x = x0 + it * W + at.x;
+    T* y = y0 + it * W + at.y;
+    const float2* f = table + at.row * a.pairs + (INTER ? it * W / 2 : it * W);
+    const int other = INTER ? 1 : a.pairs;  // distance of a pair's second element
+    P u = *reinterpret_cast<const P*>(x);
+    if (kPartner) {
+      P w = *reinterpret_cast<const P*>(x + other);
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        const unsigned i = u0 + k * lanes;
-        if (i >= units) continue;
-        r[k] = i / nheads, h[k] = i - r[k] * nheads;
-        const T* p = x + r[k] * a.x_row + h[k] * a.x_head;
-        u[k] = *reinterpret_cast<const P*>(p);
-        if (kPartner && turn) w[k] = *reinterpret_cast<const P*>(p + other);
+      for (int j = 0; j < V; ++j) {
+        const float m = to_f32(u.v[j]), n = to_f32(w.v[j]);
+        u.v[j] = from_f32<T>(m * f[j].x - n * f[j].y);
+        w.v[j] = from_f32<T>(m * f[j].y + n * f[j].x);
       }
+      *reinterpret_cast<P*>(y + other) = w;
+    } else {
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        if (u0 + k * lanes >= units) continue;
-        T* p = y + r[k] * a.y_row + h[k] * a.y_head;
-        if (turn) {
-          const float2* cs = table + r[k] * a.pairs + (INTER ? e0 / 2 : e0);
-          if (kPartner) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const float2 f = cs[j];
-              const float m = to_f32(u[k].v[j]), n = to_f32(w[k].v[j]);
-              u[k].v[j] = from_f32<T>(m * f.x - n * f.y);
-              w[k].v[j] = from_f32<T>(m * f.y + n * f.x);
-            }
-            *reinterpret_cast<P*>(p + other) = w[k];
-          } else {
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-              const float2 f = cs[j];
-              const float m = to_f32(u[k].v[2 * j]), n = to_f32(u[k].v[2 * j + 1]);
-              u[k].v[2 * j] = from_f32<T>(m * f.x - n * f.y);
-              u[k].v[2 * j + 1] = from_f32<T>(m * f.y + n * f.x);
-            }
-          }
-        }
-        *reinterpret_cast<P*>(p) = u[k];
+      for (int j = 0; j < V / 2; ++j) {
+        const float m = to_f32(u.v[2 * j]), n = to_f32(u.v[2 * j + 1]);
+        u.v[2 * j] = from_f32<T>(m * f[j].x - n * f[j].y);
+        u.v[2 * j + 1] = from_f32<T>(m * f[j].y + n * f[j].x);
       }
     }
-  }
+    *reinterpret_cast<P*>(y) = u;
+  });
+  const int tail = a.copy_tail ? (a.dim - 2 * a.pairs) / V : 0;
+  if (tail > 0)
+    each(tail, [&](int it, const Walk& at) {
+      const int e0 = 2 * a.pairs + it * V;
+      *reinterpret_cast<P*>(y0 + at.y + e0) = *reinterpret_cast<const P*>(x0 + at.x + e0);
+    });
 }
 
 template <typename T, int V, bool INTER>
