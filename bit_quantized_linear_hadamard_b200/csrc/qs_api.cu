@@ -970,15 +970,12 @@ qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t
     return QS_ERR_RANGE;
   const int64_t need = qs_lora_workspace_bytes(M, K, R, requests);
   if (need < 0 || workspace_bytes < need) return QS_ERR_RANGE;
-  for (const void* p : {x_bf16, y_bf16, a_bf16, b_bf16, static_cast<const void*>(workspace),
-                        static_cast<const void*>(out_bf16)}) {
+  const void* tensors[6] = {x_bf16, y_bf16, a_bf16, b_bf16, workspace, out_bf16};
+  for (const void* p : tensors)
     if (!aligned16(p)) return QS_ERR_ALIGN;
-    QS_TRY(check_device_ptr(p));
-  }
-  if (scale) {
-    if (!aligned_to(scale, 4)) return QS_ERR_ALIGN;
-    QS_TRY(check_device_ptr(scale));
-  }
+  if (scale && !aligned_to(scale, 4)) return QS_ERR_ALIGN;
+  for (const void* p : tensors) QS_TRY(check_device_ptr(p));
+  if (scale) QS_TRY(check_device_ptr(scale));
   QS_TRY(check_ints(seg_start));
   QS_TRY(check_ints(seg_adapter));
   qs::lora::Args a{};
