@@ -965,7 +965,7 @@ qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t
   QS_TRY(check_rows_k(M, K));
   if (N <= 0 || N % 16 != 0 || R < 8 || R % 8 != 0 || adapters <= 0 || requests <= 0)
     return QS_ERR_SHAPE;
-  if (N > QS_MAX_ROWS || R > qs::lora::kMaxRank || adapters > QS_MAX_ROWS / (R > N ? R : N) ||
+  if (N > (1LL << 24) || R > qs::lora::kMaxRank || adapters > QS_MAX_ROWS / (R > N ? R : N) ||
       requests > QS_MAX_ROWS - M)
     return QS_ERR_RANGE;
   const int64_t need = qs_lora_workspace_bytes(M, K, R, requests);

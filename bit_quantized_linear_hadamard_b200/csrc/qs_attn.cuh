@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_16(tO + 16 * q, o);
           }
         }
-        if (m != now) {  // this group's sum moves with it
-          l = m == -INFINITY ? 0.f : l * exp2_approx((m - now) * scale2);
+        if (m != now) {  // this group's sum moves with it; before any maximum it is 0, or NaN
+          if (m != -INFINITY) l *= exp2_approx((m - now) * scale2);
           m = now;
         }
         // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int k = 0; k < kGroups; ++k) {
           const float2 v = ml[((e & 1) * kGroups + k) * kBQ + r];
-          if (v.x != -INFINITY) sum += v.y * exp2_approx((v.x - mm) * scale2);
+          sum += v.x == -INFINITY ? v.y : v.y * exp2_approx((v.x - mm) * scale2);  // 0 or NaN
         }
         // a sum of 0: no key seen; NaN goes on into the row
         const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);

@@ -596,7 +596,7 @@ QS_API qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_str
  * (in front of the first, behind the last) are left as they were.  Sums in
  * binary32; the inner one enters the outer as two bf16 numbers (2^-17).
  *   x_bf16       [M, K], K % 128 == 0, K <= QS_MAX_K
- *   y_bf16       [M, N], N % 16 == 0: the projection's output
+ *   y_bf16       [M, N], N % 16 == 0, N <= 2^24: the projection's output
  *   a_bf16       [adapters, R, K];  b_bf16 [adapters, N, R];  R % 8 == 0,
  *                8 <= R <= 128 (smaller ranks: zero rows of A)
  *   scale        [adapters] float, or NULL (1)

@@ -57,7 +57,8 @@ def randn(seed, *shape, dtype=BF16, by=1.0):
 def close(got, want, tol, what):
     got = f64(got)
     assert got.shape == want.shape, what
-    bad = ~(np.abs(got - want) <= tol)
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(got - want) <= tol)
     bad &= ~(got == want)  # infinities
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: " \
                           f"{got[bad][0]} for {want[bad][0]}"
@@ -184,6 +185,36 @@ def test_lora_sizes(M, K, N, R, requests):
 
 def test_lora_update_far_larger_than_the_projection():
     check_lora(3, 40, 512, 64, 16, [0, 40], [0], 1, by=1000.0)
+
+
+def test_lora_many_requests():
+    """More requests than a block has threads; most rows in small tiles, empty ones between."""
+    rng = np.random.default_rng(0)
+    starts = np.sort(rng.integers(0, 2000, 701))
+    starts[0], starts[-1] = 1, 1990
+    check_lora(5, 2000, 128, 48, 8, starts.tolist(), rng.integers(-1, 3, 700).tolist(), 3)
+    # 200 requests of 70 rows and more on average: large tiles, more of them than the threads that look
+    starts = np.sort(rng.integers(0, 15000, 201))
+    starts[0], starts[-1] = 0, 15000
+    check_lora(6, 15000, 128, 48, 8, starts.tolist(), rng.integers(-1, 3, 200).tolist(), 3)
+
+
+def test_lora_again_and_in_a_row():
+    """The second kernel of a call runs into the first's time: calls that follow each other at once,
+    each on the last one's output, with adapters in some rows only."""
+    x, y = randn(0, 700, 1280), randn(1, 700, 528)
+    a, b = randn(2, 3, 24, 1280, by=0.03), randn(3, 3, 528, 24)
+    st = torch.tensor([0, 300, 301, 640], dtype=torch.int32, device="cuda")
+    ids = torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda")
+    want = y.clone()
+    for _ in range(8):
+        want = qs.lora_add(want, x, a, b, st, ids, out=want.clone())
+        torch.cuda.synchronize()
+    got = y.clone()
+    for _ in range(8):
+        qs.lora_add(got, x, a, b, st, ids)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
 
 
 def test_lora_bad_requests_are_left_out():
@@ -382,6 +413,52 @@ def test_attention_views_and_shared_heads():
     assert torch.equal(wide[:, :, 1::2], got) and (wide[:, :, ::2] == 4).all()
     one_k, one_v = k[:1, :, :1].expand(B, L, H, D), v[:1, :, :1].expand(B, L, H, D)
     check_attention(q, one_k, one_v, blocks)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Lq,T", [(200, 6), (1, 6)])
+def test_attention_nan_and_infinity_go_where_they_belong(D, Lq, T):
+    """A NaN query row is NaN alone; a NaN key makes the rows that list its block NaN, wherever in
+    the list it comes; a score of +inf makes its row NaN (inf - inf), as softmax does."""
+    q, k, v = randn(0, 1, Lq, 3, D), randn(1, 1, 64 * T, 3, D), randn(2, 1, 64 * T, 3, D)
+    blocks = torch.arange(T, dtype=torch.int32, device="cuda").expand(1, 3, -(-Lq // 128), T).contiguous()
+    clean, clse = qs.block_attention(q, k, v, blocks)
+    bad = q.clone()
+    bad[0, 0, 0, 5] = float("nan")
+    got, lse = qs.block_attention(bad, k, v, blocks)
+    assert got[0, 0, 0].isnan().all() and lse[0, 0, 0].isnan()
+    got[0, 0, 0], lse[0, 0, 0] = clean[0, 0, 0], clse[0, 0, 0]
+    assert torch.equal(got, clean) and torch.equal(lse, clse)
+    for row in (0, 64 * T - 1, 64 * (T // 2)):
+        bad = k.clone()
+        bad[0, row, 1, 0] = float("nan")
+        got, lse = qs.block_attention(q, bad, v, blocks)
+        assert got[:, :, 1].isnan().all() and lse[:, 1].isnan().all()
+        assert torch.equal(got[:, :, ::2], clean[:, :, ::2]) and torch.equal(lse[:, ::2], clse[:, ::2])
+    bad = k.clone()
+    bad[0, 64:192, 1] = float("nan")  # two whole blocks, one tile
+    got, lse = qs.block_attention(q, bad, v, blocks)
+    assert got[:, :, 1].isnan().all() and lse[:, 1].isnan().all()
+    bad, big = k.clone(), q.clone()
+    bad[0, 70, 2, :], big[0, 0, 2, :] = float("inf"), 1.0
+    got, lse = qs.block_attention(big, bad, v, blocks)
+    assert got[0, 0, 2].isnan().all() and lse[0, 2, 0].isnan()
+    assert torch.equal(got[:, :, :2], clean[:, :, :2])
+
+
+def test_attention_at_once_on_two_streams():
+    q, k, v = randn(0, 2, 300, 4, 128), randn(1, 2, 700, 2, 128), randn(2, 2, 700, 2, 128)
+    blocks = torch.tensor(some_blocks(0, 2, 4, 300, 700, 7), device="cuda")
+    one = torch.tensor(some_blocks(1, 2, 4, 1, 700, 11), device="cuda")
+    want, token = qs.block_attention(q, k, v, blocks), qs.block_attention(q[:, :1], k, v, one)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [[qs.block_attention(q, k, v, blocks, stream=s), qs.block_attention(q[:, :1], k, v, one, stream=s)]
+           for _ in range(5) for s in streams]
+    torch.cuda.synchronize()
+    for a, b in got:
+        for p, r in zip((*a, *b), (*want, *token)):
+            assert torch.equal(p, r)
 
 
 def test_attention_long_list_is_cut():
