@@ -180,7 +180,7 @@ def _cuda(t, dtype, name):
         return
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -844,6 +844,13 @@ def linear(x, w_packed, w_scale, bias, bits: int, alpha: float = 1.0, workspace=
     return out
 
 
+def _empty_like(t, stream):
+    """A contiguous tensor of t's shape and type, as `_empty`."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _empty(shape, dtype, device, stream):
     """A tensor for a kernel on `stream` (None: the current one), allocated on that stream: memory
     that is freed while the kernel runs then goes to later work of the same stream only."""
@@ -912,7 +919,7 @@ def rope(x, positions, inv_freq, pair_axis=None, interleaved: bool = True, scale
     place); by default a new contiguous tensor."""
     if out is None:
         _view(x, "x", _ROPE_DTYPES, 3)
-        out = _empty(x.shape, x.dtype, x.device, stream)
+        out = _empty_like(x, stream)
     flags = (QS_ROPE_INTERLEAVED if interleaved else 0) | (QS_ROPE_INVERSE if inverse else 0)
     qs_rope(x, positions, inv_freq, out, pair_axis, scale, flags, stream)
     return out
@@ -983,7 +990,7 @@ def block_attention(q, k, v, blocks, scale: float | None = None, causal: bool = 
     _view(q, "q")
     B, Lq, Hq, D = q.shape
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = _empty_like(q, stream)
     if lse is None:
         lse = _empty((B, Hq, Lq), torch.float32, q.device, stream)
     if workspace is None:

@@ -352,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the kernel that joins the parts may come onto the GPU; it waits for this one's end
+  if (a.splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // After a wait that gave up, a thread waits for nothing more and leaves its loops; no barrier
   // but the block's last one is unbounded.
@@ -391,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int off = it.kl - it.ql;  // causal: row i sees keys up to i + off
       const int limit = a.causal ? min(it.kl, row + off + 1) : it.kl;    // keys this row sees
       const int full = a.causal ? min(it.kl, it.row0 + off + 1) : it.kl; // keys every row sees
+      // a warp without a valid row only keeps step: with one query token three of four are
+      const bool idle = it.row0 + 32 * quarter >= it.ql;
       float m = -INFINITY, l = 0.f;
       // tiles of this group: those with (g0 + t) % 3 == group
       for (int t = (group + kGroups - static_cast<int>(g0 % kGroups)) % kGroups; t < n; t += kGroups) {
@@ -404,8 +408,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float old = t > 0 ? maxima[from * kBQ + r] : -INFINITY;
         wait(C::kSFull + group, ph, kErrWaitEpilogue);
         __syncwarp();
-        tc_fence_after();
         const int2 tile = tile_ring[g % kTileRing];
+        // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
+        // (behind the tensor's end the copies have filled in zeros already)
+        if (it.kl < a.Lk &&
+            (tile.x + kBK > it.kl || (tile.y < it.kl && tile.y + kBK > it.kl))) {
+          const int slot = static_cast<int>(g % C::kStages);
+          wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
+          const int key = r < kBK ? tile.x + r : tile.y + r - kBK;  // this thread's row of V
+          if (ok && key >= it.kl)
+            for (int d = 0; d < C::kHalves; ++d)
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(sp + C::kOffV + slot * C::kOp + d * C::kHalf + r * 128 +
+                                          16 * k) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          // a warp's arrival for the first block of P says that its rows are done
+        }
+        if (idle) {  // its rows of P and O stay what they are, and are not written out
+          if (lane == 0) {
+            mbar_arrive(bar(C::kMReady + group * kGroupWarps + quarter));
+            mbar_arrive(bar(C::kPFull + 2 * group));
+            mbar_arrive(bar(C::kPFull + 2 * group + 1));
+          }
+          continue;
+        }
+        tc_fence_after();
         const bool masked = tile.x + kBK > full || tile.y + kBK > full;
         // two sets of registers: the next 32 scores are on their way while these are looked at
         uint32_t sa[32], sb[32];
@@ -448,23 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m != now) {  // this group's sum moves with it; before any maximum it is 0, or NaN
           if (m != -INFINITY) l *= exp2_approx((m - now) * scale2);
           m = now;
-        }
-        // rows of V behind the keys may hold anything, and 0 times a NaN is one: they become 0
-        // (behind the tensor's end the copies have filled in zeros already)
-        if (it.kl < a.Lk &&
-            (tile.x + kBK > it.kl || (tile.y < it.kl && tile.y + kBK > it.kl))) {
-          const int slot = static_cast<int>(g % C::kStages);
-          wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
-          const int key = r < kBK ? tile.x + r : tile.y + r - kBK;  // this thread's row of V
-          if (ok && key >= it.kl)
-            for (int d = 0; d < C::kHalves; ++d)
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(sp + C::kOffV + slot * C::kOp + d * C::kHalf + r * 128 +
-                                          16 * k) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          // both halves' products read rows that other warps of the group have cleared: each
-          // warp's arrival for the first half says that its rows are done
         }
         // P of a block goes to the second product as soon as it is written
         const auto give_half = [&](int half) {
@@ -830,6 +841,7 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   const int64_t parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
   const int64_t flat = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (flat >= parts) return;
   const int lane = threadIdx.x & 31;
   const int64_t row = flat % a.Lq;
@@ -914,8 +926,8 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   const cudaError_t l = cudaGetLastError();
   if (l != cudaSuccess || a.splits == 1) return l;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
-  join_kernel<D, F16><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_behind(join_kernel<D, F16>, dim3(static_cast<unsigned>((rows + 7) / 8)), 256, 0,
+                       stream, a);
 }
 
 }  // namespace attn

@@ -635,18 +635,6 @@ cudaError_t launch_shrink_large(const Args& a, const Plan& p, cudaStream_t strea
   return cudaGetLastError();
 }
 
-template <typename... Params>
-cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, int smem,
-                          cudaStream_t stream, Params... params) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream, cfg.attrs = &attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, params...);
-}
-
 template <int KH>
 cudaError_t launch_expand_large(const Args& a, const Plan& p, cudaStream_t stream) {
   using C = ExpandCfg<KH>;

@@ -149,9 +149,15 @@ __device__ __forceinline__ unsigned long long score_key(double s) {
   return v < 0 ? ~u : u | 0x8000000000000000ull;
 }
 
-// OWN: the query means are formed here.
+// OWN: the query means are formed here, in blocks of more threads: with few query blocks it is the
+// way of one of them that counts.
+template <bool OWN>
+constexpr int kSelectThreads = OWN ? 512 : kThreads;
+
 template <int D, bool F16, bool OWN>
-__global__ void __launch_bounds__(kThreads, OWN ? 2 : 3) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelectThreads<OWN>, OWN ? 1 : 3)
+    select_kernel(const SelectArgs a) {
+  constexpr int kThreads = kSelectThreads<OWN>, kWarps = kThreads / 32;
   extern __shared__ __align__(16) double qm[];  // query means [8][D], behind them the keys [rows][nk]
   unsigned long long* keys = reinterpret_cast<unsigned long long*>(qm + kRows * D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 2 : 3) select_kernel(const Sel
   __syncthreads();
 
   // the T highest of each row's visible blocks: the largest threshold that T keys reach, found
-  // bit by bit from the top, ended as soon as exactly T reach it
+  // from its top bits down, ended as soon as exactly T reach it
   if (warp >= a.rows || i0 + warp >= a.nq) return;
   const int i = i0 + warp;
   const int64_t row0 = static_cast<int64_t>(i) * QS_BLOCK_Q;
@@ -228,25 +234,25 @@ __global__ void __launch_bounds__(kThreads, OWN ? 2 : 3) select_kernel(const Sel
     if (j < a.first || j >= n - a.last) key[j] = ~0ull;
   __syncwarp();
   unsigned long long least = 0ull;
-  int ties = 0;  // blocks with exactly `least` that are taken; -1: all
+  int ties = -1;  // blocks with exactly `least` that are taken; -1: all
   if (n > a.T) {
     int above = 0;  // keys above `least` at the end
     bool exact = false;
-    for (int bit = 63; bit >= 0 && !exact; --bit) {
-      const unsigned long long at = least | (1ull << bit);
-      int count = 0;
-      for (int j = lane; j < n; j += 32) count += key[j] >= at;
-      count = __reduce_add_sync(0xffffffffu, count);
-      if (count >= a.T) {
-        least = at;
-        exact = count == a.T;
-      } else {
-        above = count;
+    for (int bit = 62; bit >= 0 && !exact; bit -= 2) {  // two bits at a time
+      int count[3] = {0, 0, 0};  // of the three numbers that the two bits may become besides 0
+      for (int j = lane; j < n; j += 32) {
+        const unsigned long long v = key[j];
+#pragma unroll
+        for (unsigned long long c = 0; c < 3; ++c) count[c] += v >= (least | ((c + 1) << bit));
       }
+#pragma unroll
+      for (int c = 0; c < 3; ++c) count[c] = __reduce_add_sync(0xffffffffu, count[c]);
+      const unsigned long long most = count[2] >= a.T ? 3 : count[1] >= a.T ? 2 : count[0] >= a.T ? 1 : 0;
+      if (most < 3) above = count[most];
+      exact = most > 0 && count[most - 1] == a.T;
+      least |= most << bit;
     }
-    ties = exact ? -1 : a.T - above;
-  } else {
-    ties = -1;
+    if (!exact) ties = a.T - above;
   }
   int32_t* out = a.blocks + ((static_cast<int64_t>(b) * a.Hq + h) * a.nq + i) * a.T;
   int filled = 0, tied = 0;
@@ -295,7 +301,8 @@ cudaError_t launch_select(SelectArgs a, float* workspace, cudaStream_t stream) {
                                              kMaxSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.nq + a.rows - 1) / a.rows, a.Hq, a.B);
-  kern<<<grid, kThreads, static_cast<size_t>(smem()), stream>>>(a);
+  kern<<<grid, own ? kSelectThreads<true> : kSelectThreads<false>, static_cast<size_t>(smem()),
+         stream>>>(a);
   return cudaGetLastError();
 }
 
