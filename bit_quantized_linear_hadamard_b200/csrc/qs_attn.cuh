@@ -524,10 +524,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) wait(C::kPvDone + last, ((g0 - 1) / kGroups) & 1, kErrWaitEpilogue);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
+        // O into registers first: the next item's products wait for its place
+        uint32_t o[2][32];
+        tmem_ld_32x32b_x32(tO + 64 * half, o[0]);
+        tmem_ld_32x32b_x32(tO + 64 * half + 32, o[1]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (n > 0 && lane == 0) mbar_arrive(bar(C::kOFree));
         float mm = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) mm = fmaxf(mm, ml[((e & 1) * kGroups + k) * kBQ + r].x);
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < kGroups; ++k) {
           const float2 v = ml[((e & 1) * kGroups + k) * kBQ + r];
           sum += v.x == -INFINITY ? v.y : v.y * exp2_approx((v.x - mm) * scale2);  // 0 or NaN
@@ -538,49 +546,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
         const bool write = row < it.ql;
         // A whole block goes through shared memory (its Q is done with) and out by TMA: single
-        // rows from the threads would take 2048 line accesses of the L1.  The loop is kept short:
-        // code that runs once per item comes from beyond the instruction cache, and unrolled it
-        // took longer to fetch than to run.
+        // rows from the threads would take 2048 line accesses of the L1.
         const bool whole = n > 0 && it.row0 + kBQ <= it.ql && a.splits == 1;
-        uint8_t* stage = sp + C::kOffQ + qb * C::kOp + half * C::kHalf + r * 128;
-        uint16_t* direct = static_cast<uint16_t*>(a.out) + it.b * a.o_batch + row * a.o_row +
-                           it.h * a.o_head + 64 * half;
-        float* part = a.part + (it.split * parts + flat) * D + 64 * half;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[16];
-          tmem_ld_16(tO + 64 * half + 16 * k, o);
-          tmem_wait_ld();
+        const auto value = [&](int k) {
+          return inv == 0.f ? 0.f : __uint_as_float(o[k / 32][k % 32]) * inv;
+        };
+        if (a.splits > 1) {
+          if (write) {
+            float4* part = reinterpret_cast<float4*>(a.part + (it.split * parts + flat) * D + 64 * half);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            o[j] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
-          if (a.splits > 1) {
-            if (write)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                reinterpret_cast<uint4*>(part)[4 * k + j] =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              o[j] = pack2<F16>(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]);
-            const uint4 hi = make_uint4(o[4], o[5], o[6], o[7]);
-            if (whole) {
-              *reinterpret_cast<uint4*>(stage + 16 * ((2 * k) ^ (r & 7))) = lo;
-              *reinterpret_cast<uint4*>(stage + 16 * ((2 * k + 1) ^ (r & 7))) = hi;
-            } else if (write) {
-              reinterpret_cast<uint4*>(direct)[2 * k] = lo;
-              reinterpret_cast<uint4*>(direct)[2 * k + 1] = hi;
-            }
+            for (int k = 0; k < 16; ++k)
+              part[k] = make_float4(value(4 * k), value(4 * k + 1), value(4 * k + 2), value(4 * k + 3));
           }
-          __syncwarp();
+        } else {
+          uint8_t* stage = sp + C::kOffQ + qb * C::kOp + half * C::kHalf + r * 128;
+          uint4* direct = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + it.b * a.o_batch +
+                                                   row * a.o_row + it.h * a.o_head + 64 * half);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack2<F16>(value(8 * k + 2 * j), value(8 * k + 2 * j + 1));
+            const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+            if (whole)
+              *reinterpret_cast<uint4*>(stage + 16 * (k ^ (r & 7))) = v;
+            else if (write)
+              direct[k] = v;
+          }
         }
-        tc_fence_before();
         if (whole) fence_proxy_async_smem();
         __syncwarp();
         if (n > 0 && lane == 0) {
-          mbar_arrive(bar(C::kOFree));
           // the last of the group's warps sends the 64 columns off, or gives the buffer back
           __threadfence_block();
           if ((atomicAdd(&staged_warps[half], 1) & (kGroupWarps - 1)) == kGroupWarps - 1) {
