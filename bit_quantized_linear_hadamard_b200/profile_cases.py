@@ -22,6 +22,10 @@ Cases:
   quant           qs_quant_act at any shape and width (--K, --bits, --alpha, --byte-codes)
   gemm            qs_qlinear_mixed at any shape and widths (--K, --N, --bits-x, --bits-w,
                   --byte-codes: 4-bit activation codes stored one per byte)
+  rope            qs_rope on the query and key heads (80 of 128) of qkv rows, three axes
+  lora            qs_lora_add of two requests' rank-64 adapters beside the FFN up-projection
+  select          qs_block_means and qs_block_select of 8 heads, 77 blocks of 512 at 32760 tokens
+  attention       qs_block_attention of 4 heads over 15 % of the key blocks
 """
 
 from __future__ import annotations
@@ -48,7 +52,8 @@ def main(argv=None) -> None:
     p.add_argument("case", choices=["sd4_gemm_e4m3", "sd4_gemm_e4m3_tiles", "sd4_gemm_codes",
                                     "sd4_quant_e4m3",
                                     "gbs_update", "gelu", "gemm_w8a8", "gemm_w4a8",
-                                    "gemm_bgr", "quant", "gemm"])
+                                    "gemm_bgr", "quant", "gemm", "rope", "lora", "select",
+                                    "attention"])
     p.add_argument("--tokens", type=int, default=None)
     p.add_argument("--K", type=int, default=K)
     p.add_argument("--N", type=int, default=N)
@@ -118,6 +123,40 @@ def main(argv=None) -> None:
         out = torch.empty((M, a.N), dtype=torch.bfloat16, device="cuda")
         run = lambda: qs.qs_qlinear_mixed(xp, xs, sx, wp, ws, a.bits_w, b, M, a.N, a.K,  # noqa: E731
                                           out)
+    elif a.case == "rope":
+        M = a.tokens or 8192
+        g = torch.Generator(device="cuda").manual_seed(0)
+        qkv = torch.randn(M, 3 * K, device="cuda", generator=g).to(torch.bfloat16)
+        inv, axis, _ = qs.rope_frequencies(128, axes=(44, 42, 42))
+        row = torch.arange(M, device="cuda")
+        pos = torch.stack([row // 1560, row // 52 % 30, row % 52], 1).contiguous()
+        qk = qkv[:, : 2 * K].view(M, 80, 128)
+        out = torch.empty((M, 80, 128), dtype=torch.bfloat16, device="cuda")
+        run = lambda: qs.rope(qk, pos, inv, axis, out=out)  # noqa: E731
+    elif a.case == "lora":
+        M = a.tokens or 8192
+        x, _, _ = _inputs(M)
+        g = torch.Generator(device="cuda").manual_seed(3)
+        y = torch.randn(M, N, device="cuda", generator=g).to(torch.bfloat16)
+        la = (torch.randn(2, 64, K, device="cuda", generator=g) * 0.014).to(torch.bfloat16)
+        lb = (torch.randn(2, N, 64, device="cuda", generator=g) * 0.06).to(torch.bfloat16)
+        starts = torch.tensor([0, M // 2, M], dtype=torch.int32, device="cuda")
+        ids = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        out = torch.empty_like(y)
+        run = lambda: qs.lora_add(y, x, la, lb, starts, ids, out=out)  # noqa: E731
+    elif a.case in ("select", "attention"):
+        M = a.tokens or 32760
+        H = 8 if a.case == "select" else 4
+        g = torch.Generator(device="cuda").manual_seed(4)
+        q, k, v = (torch.randn(1, M, H, 128, device="cuda", generator=g).to(torch.bfloat16)
+                   for _ in range(3))
+        count = max(1, round(0.15 * -(-M // qs.QS_BLOCK_K)))
+        if a.case == "select":
+            run = lambda: qs.block_select(q, qs.block_means(k), count, M)  # noqa: E731
+        else:
+            blocks = qs.block_select(q, qs.block_means(k), count, M)
+            out, lse = torch.empty_like(q), torch.empty((1, H, M), device="cuda")
+            run = lambda: qs.block_attention(q, k, v, blocks, out=out, lse=lse)  # noqa: E731
     elif a.case == "gelu":
         M = a.tokens or 4096
         g = torch.Generator(device="cuda").manual_seed(2)
