@@ -212,17 +212,25 @@ cudaError_t launch_t(Args a, int sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <typename T, int V>
+bool accesses_fit(const Args& a, bool interleaved) {
+  const auto multiple = [](int64_t v) { return v % V == 0; };
+  const uintptr_t bytes = V * sizeof(T) - 1;
+  return (reinterpret_cast<uintptr_t>(a.x) & bytes) == 0 &&
+         (reinterpret_cast<uintptr_t>(a.y) & bytes) == 0 && multiple(a.x_row) &&
+         multiple(a.x_head) && multiple(a.y_row) && multiple(a.y_head) &&
+         multiple(interleaved ? 2 * a.pairs : a.pairs) && multiple(a.dim);
+}
+
+// The widest accesses that the views allow: 16 bytes, two elements, one.
 template <typename T>
 cudaError_t launch(const Args& a, bool interleaved, int sms, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(T);
-  const auto multiple = [](int64_t v) { return v % V == 0; };
-  const bool wide = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
-                    (reinterpret_cast<uintptr_t>(a.y) & 15u) == 0 && multiple(a.x_row) &&
-                    multiple(a.x_head) && multiple(a.y_row) && multiple(a.y_head) &&
-                    multiple(interleaved ? 2 * a.pairs : a.pairs) && multiple(a.dim);
-  if (interleaved)
-    return wide ? launch_t<T, V, true>(a, sms, stream) : launch_t<T, 1, true>(a, sms, stream);
-  return wide ? launch_t<T, V, false>(a, sms, stream) : launch_t<T, 1, false>(a, sms, stream);
+  if (accesses_fit<T, V>(a, interleaved))
+    return interleaved ? launch_t<T, V, true>(a, sms, stream) : launch_t<T, V, false>(a, sms, stream);
+  if (accesses_fit<T, 2>(a, interleaved))
+    return interleaved ? launch_t<T, 2, true>(a, sms, stream) : launch_t<T, 2, false>(a, sms, stream);
+  return interleaved ? launch_t<T, 1, true>(a, sms, stream) : launch_t<T, 1, false>(a, sms, stream);
 }
 
 }  // namespace rope

@@ -572,7 +572,7 @@ typedef struct {
  *               same strides; otherwise the two must not share elements.  With
  *               16-byte aligned pointers, strides and head dimensions that
  *               are multiples of 16 bytes (rot_dim, or rot_dim/2 in halves,
- *               too) accesses are 16 bytes wide, else single elements.
+ *               too) accesses are 16 bytes wide, else two elements or one.
  *   rot_dim     even, 2 .. head_dim;  head_dim <= 1024
  *   positions   [rows, axes] int64 (device, contiguous);  axes 1 .. 8
  *   pair_axis   [rot_dim/2] int32 (device) or NULL (axis 0 for all); a value
