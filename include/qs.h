@@ -544,7 +544,8 @@ QS_API qs_status qs_gelu_bf16(const void* x_bf16, int64_t n, void* y_bf16, void*
  * (its "Resumen técnico" §2.B, §4); the pages give no kernel of either, the
  * definitions here are this library's.  All are forward (serving) operators.
  *
- * They take views: strides are in ELEMENTS, the last dimension is contiguous.
+ * Rotary positions, means, selection and attention take views: strides are in
+ * ELEMENTS, the last dimension is contiguous.
  */
 typedef enum { QS_BF16 = 0, QS_F16 = 1, QS_F32 = 2 } qs_dtype;
 
@@ -606,7 +607,8 @@ QS_API qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_str
  *                qs_device_error report QS_ERR_RANGE.
  *   workspace    qs_lora_workspace_bytes(M, K, R, requests) bytes of device
  *                scratch, 16-byte aligned (-1 for rejected arguments)
- *   out_bf16     [M, N]; may be y_bf16 itself
+ *   out_bf16     [M, N]; may be y_bf16 itself, else it and the workspace must
+ *                not overlap the other arguments
  */
 QS_API int64_t qs_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t requests);
 QS_API qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t K,
