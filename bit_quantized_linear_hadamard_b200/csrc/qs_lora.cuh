@@ -14,7 +14,7 @@
 //
 // Both are bound by HBM: x once, y and out once.
 //
-// Shrink, tiles of 128 rows (requests of 64 rows and more on average): tcgen05 MMAs of 128 x R on
+// Shrink, tiles of 128 rows (long requests, plan() has the rule): tcgen05 MMAs of 128 x R on
 // a ring of TMA stages of 64 k; two CTAs per SM keep 190 KB in flight.  Tiles of 16 rows (a token
 // or a few per request): mma.sync, the block's warps share K, operands from global memory straight
 // to fragments.  A fragment only needs A and B to use the same order of k, so a thread takes 8
@@ -65,7 +65,15 @@ struct Plan {
 
 inline Plan plan(int64_t M, int64_t K, int64_t R, int64_t requests) {
   Plan p;
-  p.large = M / requests >= kLargeRows / 2;
+  // Large tiles cost a fixed time each and pay from full ones on; small ones form up to 64 ranks
+  // in registers and read y and B once for each 16 rows.  By rows per request (uneven lengths),
+  // large / small, us, M 8192, K and N 5120: R 16: 119 / 84 at 128, 88 / 84 at 1024; R 32: 118 /
+  // 95 at 128, 107 / 93 at 256 (K 13824: 129 / 137), 40 / 64 at M 4096 of one request; R 64:
+  // 247 / 219 at 16, 167 / 165 at 32, 122 / 155 at 128; R 128: 246 / 297 at 32.  Little x in all:
+  // 23 / 19 at M 512 R 32, 20 / 16 at M 1024 K 1536 R 48.
+  const int64_t rows_each = M / requests;
+  p.large = M * K >= (1 << 22) &&
+            (R > 32 ? rows_each >= kLargeRows / 4 : rows_each * R * R >= (1 << 18));
   const int rows = p.large ? kLargeRows : kSmallRows;
   p.tiles = M / rows + requests;
   const int64_t blocks = p.large ? p.tiles : p.tiles * ((R + kGroup - 1) / kGroup);

@@ -279,7 +279,8 @@ cudaError_t launch_means(const MeanArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Query means formed on the way: up to this many query blocks in all.
+// Query means formed on the way: up to this many query blocks in all.  Formed on the way / apart,
+// us, D 128: 32.5 / 43.2 at 256 blocks, 36.5 / 43.3 at 1024, 74.3 / 68.1 at 2048.
 constexpr int64_t kOwnMeans = 1024;
 
 template <int D, bool F16>

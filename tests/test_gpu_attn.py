@@ -183,6 +183,15 @@ def test_lora_sizes(M, K, N, R, requests):
     check_lora(M, M, K, N, R, starts, [(3 * i) % 5 - 1 for i in range(requests)], 4, scaled=M % 2 == 0)
 
 
+@pytest.mark.parametrize("R,M,K", [(8, 33000, 128), (16, 9300, 512), (24, 3300, 1280), (32, 2500, 1792),
+                                   (40, 2000, 2176), (64, 1100, 4096), (128, 1100, 4096)])
+def test_lora_long_requests(R, M, K):
+    """Tiles of 128 rows at every rank: uneven lengths, rows in front, behind and without an adapter."""
+    starts = [1, 2, M // 3 + 5, M // 3 + 5, M - 130, M - 2] if R > 32 else [1, M // 3 + 5, M - 130, M - 2]
+    ids = [1, 0, 1, 2, -1] if R > 32 else [2, 0, -1]
+    check_lora(50 + R, M, K, 80, R, starts, ids, 3, in_place=R % 16 == 0)
+
+
 def test_lora_update_far_larger_than_the_projection():
     check_lora(3, 40, 512, 64, 16, [0, 40], [0], 1, by=1000.0)
 
@@ -196,7 +205,7 @@ def test_lora_many_requests():
     # 200 requests of 70 rows and more on average: large tiles, more of them than the threads that look
     starts = np.sort(rng.integers(0, 15000, 201))
     starts[0], starts[-1] = 0, 15000
-    check_lora(6, 15000, 128, 48, 8, starts.tolist(), rng.integers(-1, 3, 200).tolist(), 3)
+    check_lora(6, 15000, 384, 48, 40, starts.tolist(), rng.integers(-1, 3, 200).tolist(), 3)
 
 
 def test_lora_again_and_in_a_row():
