@@ -42,20 +42,6 @@ inline bool make_tensor_map_2d(CUtensorMap* map, const void* base, uint64_t row_
   return r == CUDA_SUCCESS;
 }
 
-// A launch that may start before the kernel in front of it in the stream has ended (programmatic
-// dependent launch); the kernel waits for that end itself, in every block.
-template <typename... Params>
-cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, int smem,
-                          cudaStream_t stream, Params... params) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream, cfg.attrs = &attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, params...);
-}
-
 inline int sm_count() {
   static int cached[64] = {0};
   int dev = 0;

@@ -34,6 +34,7 @@
 
 #include "qs.h"
 #include "qs_host.cuh"
+#include "qs_launch.cuh"
 #include "qs_ptx.cuh"
 
 namespace qs {
