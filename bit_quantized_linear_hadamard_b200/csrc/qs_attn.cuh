@@ -83,7 +83,8 @@ struct Cfg {
     const auto in = [&](int first, int n) { return i >= first && i < first + n; };
     if (in(kPFull, 2 * kGroups)) return kGroupWarps;
     if (in(kSFull, kGroups)) return 2;                            // formed, and its keys known
-    if (i == kOFree || i == kMlFull) return kGroups * kGroupWarps;
+    if (i == kMlFull) return kGroups * kGroupWarps;
+    if (i == kOFree) return kHalves * kGroupWarps;                // the writers' warps only
     if (in(kQFree, 2)) return 1 + kHalves;                        // scores formed, output staged
     if (in(kItemEmpty, kItemRing)) return kGroups * kGroupWarps + 2;
     return 1;
@@ -525,7 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) wait(C::kPvDone + last, ((g0 - 1) / kGroups) & 1, kErrWaitEpilogue);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        // O into registers first: the next item's products wait for its place
+        // O into registers first: the next item's products wait for its place.  Only the writers
+        // give it back: a group that does not read O may be an item ahead, and its arrival would
+        // then stand for one that is still to come
         uint32_t o[2][32];
         tmem_ld_32x32b_x32(tO + 64 * half, o[0]);
         tmem_ld_32x32b_x32(tO + 64 * half + 32, o[1]);
@@ -608,8 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[flat] = lse;
         }
         __syncwarp();
-      } else {
-        if (n > 0 && lane == 0) mbar_arrive(bar(C::kOFree));
       }
     }
     see_off();

@@ -455,6 +455,38 @@ def test_attention_nan_and_infinity_go_where_they_belong(D, Lq, T):
     assert torch.equal(got[:, :, :2], clean[:, :, :2])
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("causal,B,Lq,Lk,Hq,Hkv,T,ragged,copies", [
+    (False, 1, 640, 300, 4, 2, 2, False, 40), (False, 1, 384, 512, 4, 4, 6, False, 60), (True, 2, 257, 500, 4, 2, 8, True, 30),
+    (False, 3, 130, 900, 4, 1, 5, True, 30), (True, 1, 700, 700, 4, 4, 7, False, 30)])
+def test_attention_more_items_than_processors(monkeypatch, dtype, D, causal, B, Lq, Lk, Hq, Hkv, T, ragged, copies):
+    """Four and more items for each CTA, of one tile, three and others: O, both Q buffers, the sums and
+    the rings serve one item after another, and again the same to the last bit.  The batch is `copies`
+    of the same B sequences, which the oracle sees once."""
+    again = lambda t: t.repeat(copies, 1, 1, 1)  # noqa: E731
+    q = again(randn(Lq, B, Lq, Hq, D, dtype=dtype, by=2.0))
+    k, v = again(randn(Lk, B, Lk, Hkv, D, dtype=dtype)), again(randn(Lk + 1, B, Lk, Hkv, D, dtype=dtype))
+    ql = [Lq - 61 * b for b in range(B)] * copies if ragged else None
+    kl = [Lk - 67 * b for b in range(B)] * copies if ragged else None
+    blocks = np.tile(some_blocks(T, B, Hq, Lq, Lk, T, holes=ragged), (copies, 1, 1, 1))
+    assert blocks.size // T >= 600
+    real = O.block_attention
+
+    def once(q, k, v, blocks, scale, causal, q_len, k_len, out, lse):
+        n = [None if t is None else t[:B] for t in (q_len, k_len)]
+        want = real(q[:B], k[:B], v[:B], blocks[:B], scale, causal, *n, out[:B], lse[:B])
+        return [np.tile(t, (copies,) + (1,) * (t.ndim - 1)) for t in want]
+
+    monkeypatch.setattr(O, "block_attention", once)
+    got, lse = check_attention(q, k, v, blocks, causal=causal, q_len=ql, k_len=kl)
+    ints = lambda t: None if t is None else torch.tensor(t, dtype=torch.int32, device="cuda")  # noqa: E731
+    dev = ints(blocks), ints(ql), ints(kl)
+    for _ in range(10):
+        o, z = qs.block_attention(q, k, v, dev[0], causal=causal, q_len=dev[1], k_len=dev[2], out=torch.full_like(got, 9.0),
+                                  lse=torch.full_like(lse, 9.0))
+        assert torch.equal(o, got) and torch.equal(z, lse)
+
+
 def test_attention_at_once_on_two_streams():
     q, k, v = randn(0, 2, 300, 4, 128), randn(1, 2, 700, 2, 128), randn(2, 2, 700, 2, 128)
     blocks = torch.tensor(some_blocks(0, 2, 4, 300, 700, 7), device="cuda")
