@@ -541,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kGroups; ++k) mm = fmaxf(mm, ml[((e & 1) * kGroups + k) * kBQ + r].x);
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
-          const float2 v = ml[((e & 1) * kGroups + k) * kBQ + r];
+          // in the order of the item's tiles, so that it does not matter where a CTA meets it
+          const float2 v = ml[((e & 1) * kGroups + (g0 - n + k) % kGroups) * kBQ + r];
           sum += v.x == -INFINITY ? v.y : v.y * exp2_approx((v.x - mm) * scale2);  // 0 or NaN
         }
         // a sum of 0: no key seen; NaN goes on into the row

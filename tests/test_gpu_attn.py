@@ -479,6 +479,8 @@ def test_attention_more_items_than_processors(monkeypatch, dtype, D, causal, B, 
 
     monkeypatch.setattr(O, "block_attention", once)
     got, lse = check_attention(q, k, v, blocks, causal=causal, q_len=ql, k_len=kl)
+    for t in (got, lse):
+        assert torch.equal(t, t[:B].repeat(copies, *[1] * (t.dim() - 1)))
     ints = lambda t: None if t is None else torch.tensor(t, dtype=torch.int32, device="cuda")  # noqa: E731
     dev = ints(blocks), ints(ql), ints(kl)
     for _ in range(10):
