@@ -131,6 +131,13 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The largest, or NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) {
   return __ldg(reinterpret_cast<const uint4*>(p));
 }
@@ -347,6 +354,26 @@ __device__ __forceinline__ void load_t(const Args& a, int64_t row, int k, float 
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// The sums of `count` columns from n on of one row that came out as NaN, formed again from t in one
+// piece: times an infinite element of B the two parts of t give infinities of either sign, or 0 times
+// infinity, where t itself gives one infinity.  A sum that is NaN by itself stays so, and the first
+// such term ends it.
+__device__ __noinline__ void sum_again(const Args& a, int64_t row, int adapter, int n, int count,
+                                       float* sums) {
+  const float scale = a.scale ? a.scale[adapter] : 1.f;
+  for (int e = 0; e < count && n + e < a.N; ++e) {
+    if (sums[e] == sums[e]) continue;
+    const uint16_t* b = a.b + (static_cast<int64_t>(adapter) * a.N + n + e) * a.R;
+    float sum = 0.f;
+    for (int r = 0; r < a.R && sum == sum; ++r) {
+      float t = 0.f;
+      for (int i = 0; i < a.slices; ++i) t += a.part[(i * a.M + row) * a.R + r];
+      sum = fmaf(t * scale, __uint_as_float(static_cast<uint32_t>(b[r]) << 16), sum);
+    }
+    sums[e] = sum;
+  }
+}
+
 // Two k16 steps of 16 rows x 8 columns: t as tops and rest, rows g (0) and g + 8 (1) of each.
 __device__ __forceinline__ void mma_t(float (&acc)[4], const uint4 (&hi)[2], const uint4 (&lo)[2],
                                       const uint4& w) {
@@ -354,6 +381,22 @@ __device__ __forceinline__ void mma_t(float (&acc)[4], const uint4 (&hi)[2], con
   mma_bf16_16816(acc, lo[0].x, lo[1].x, lo[0].y, lo[1].y, w.x, w.y);
   mma_bf16_16816(acc, hi[0].z, hi[1].z, hi[0].w, hi[1].w, w.z, w.w);
   mma_bf16_16816(acc, lo[0].z, lo[1].z, lo[0].w, lo[1].w, w.z, w.w);
+}
+
+__device__ __forceinline__ void mma_tops(float (&acc)[4], const uint4 (&hi)[2], const uint4& w) {
+  mma_bf16_16816(acc, hi[0].x, hi[1].x, hi[0].y, hi[1].y, w.x, w.y);
+  mma_bf16_16816(acc, hi[0].z, hi[1].z, hi[0].w, hi[1].w, w.z, w.w);
+}
+
+// Whether one of the thread's sums is NaN.
+__device__ __forceinline__ bool has_nan(const float (&acc)[4][4]) {
+  float most[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    most[0] = max3_nan(most[0], acc[j][0], acc[j][1]);
+    most[1] = max3_nan(most[1], acc[j][2], acc[j][3]);
+  }
+  return isnan(most[0] + most[1]);
 }
 
 // y + the sums of four n8 tiles, as bf16.  The tiles' column order inside their 32 is permuted so
@@ -407,7 +450,8 @@ template <int KH>
 __global__ void __launch_bounds__(kExpandThreads)
     expand_large_kernel(const __grid_constant__ CUtensorMap tmY,
                         const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmO, const Args a, int chunks_each) {
+                        const __grid_constant__ CUtensorMap tmO,
+                        const __grid_constant__ Args a, int chunks_each) {
   using C = ExpandCfg<KH>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -527,6 +571,21 @@ __global__ void __launch_bounds__(kExpandThreads)
         uint32_t d[32];
         tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kCols * buf + 32 * h, d);
         tmem_wait_ld();
+        float most[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          most[0] = max3_nan(most[0], __uint_as_float(d[e]), __uint_as_float(d[e + 1]));
+          most[1] = max3_nan(most[1], __uint_as_float(d[e + 2]), __uint_as_float(d[e + 3]));
+        }
+        if (isnan(most[0] + most[1]) && r < tile.rows && ok) {
+          float sums[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sums[e] = __uint_as_float(d[e]);
+          sum_again(a, tile.row0 + r, tile.adapter, c0 + 32 * h, 32, sums);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) d[e] = __float_as_uint(sums[e]);
+        }
+        __syncwarp();
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           uint4* at = reinterpret_cast<uint4*>(y + 16 * ((4 * h + p) ^ (r & 7)));
@@ -595,16 +654,21 @@ __global__ void __launch_bounds__(kThreads) expand_small_kernel(const Args a, in
     for (int h = 0; h < 2; ++h)
       load_t(a, tile.row0 + g + 8 * h, 32 * s + 8 * c, scale, turned && g + 8 * h < tile.rows,
              hi[s][h], lo[s][h]);
-#pragma unroll 2
+  const auto there = [&](int n0, int h) { return n0 + 8 * c < a.N && g + 8 * h < tile.rows; };
+  const auto offset = [&](int n0, int h) {
+    return static_cast<int64_t>(tile.row0 + g + 8 * h) * a.N + n0 + 8 * c;
+  };
+  const auto load_y = [&](int n0, int h) {
+    return there(n0, h) ? *reinterpret_cast<const uint4*>(a.y + offset(n0, h)) : make_uint4(0, 0, 0, 0);
+  };
+  bool again = false;
+  // Twice for every rank: 20.8 for 20.1 us (64 tokens, R 16), 60.1 for 59.5 (R 128).
+  constexpr int kUnroll = KS == 1 ? 3 : KS == 2 ? 2 : 1;
+#pragma unroll kUnroll
   for (int n0 = n_begin; n0 < n_end; n0 += 32 * kWarps) {
-    const bool in = n0 + 8 * c < a.N;
-    const int64_t at = static_cast<int64_t>(tile.row0 + g) * a.N + n0 + 8 * c;
     uint4 y[2], w[KS][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      y[h] = in && g + 8 * h < tile.rows
-                 ? *reinterpret_cast<const uint4*>(a.y + at + static_cast<int64_t>(8 * h) * a.N)
-                 : make_uint4(0, 0, 0, 0);
+    for (int h = 0; h < 2; ++h) y[h] = load_y(n0, h);
     float acc[4][4] = {};
     if (turned) {
       load_b<KS>(a, tile.adapter, n0, w);
@@ -613,11 +677,40 @@ __global__ void __launch_bounds__(kThreads) expand_small_kernel(const Args a, in
 #pragma unroll
         for (int j = 0; j < 4; ++j) mma_t(acc[j], hi[s], lo[s], w[s][j]);
     }
+    const bool nan = has_nan(acc);
+    again |= nan;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (in && g + 8 * h < tile.rows)
-        *reinterpret_cast<uint4*>(a.out + at + static_cast<int64_t>(8 * h) * a.N) =
-            turned ? add_y(y[h], acc, h) : y[h];
+      if (there(n0, h) && !nan)
+        *reinterpret_cast<uint4*>(a.out + offset(n0, h)) = turned ? add_y(y[h], acc, h) : y[h];
+  }
+  // Times an infinite element of B the tops give the infinity that t does, the rest one of its own
+  // sign, or 0 times infinity: a sum of both that is NaN is the tops' alone.  Such pieces were left
+  // out above, and are formed again here: a branch in the loop cost 2 to 8 us of 20 to 35.
+  if (!__any_sync(0xffffffffu, again)) return;
+#pragma unroll 1
+  for (int n0 = n_begin; n0 < n_end; n0 += 32 * kWarps) {
+    uint4 w[KS][4];
+    float acc[4][4] = {}, top[4][4] = {};
+    load_b<KS>(a, tile.adapter, n0, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        mma_t(acc[j], hi[s], lo[s], w[s][j]);
+        mma_tops(top[j], hi[s], w[s][j]);
+      }
+    }
+    const bool nan = has_nan(acc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!there(n0, h) || !nan) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 2 * h; e < 2 * h + 2; ++e) acc[j][e] = isnan(acc[j][e]) ? top[j][e] : acc[j][e];
+      *reinterpret_cast<uint4*>(a.out + offset(n0, h)) = add_y(load_y(n0, h), acc, h);
+    }
   }
 }
 

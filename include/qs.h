@@ -595,7 +595,8 @@ QS_API qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_str
  * with i = seg_adapter[s] for the rows seg_start[s] <= m < seg_start[s+1] of
  * request s.  i = -1: no adapter, out = y there.  Rows outside every request
  * (in front of the first, behind the last) are left as they were.  Sums in
- * binary32; the inner one enters the outer as two bf16 numbers (2^-17).
+ * binary32; the inner one enters the outer as two bf16 numbers (2^-17; infinite
+ * beyond bf16's largest number, 3.39e38).
  *   x_bf16       [M, K], K % 128 == 0, K <= QS_MAX_K
  *   y_bf16       [M, N], N % 16 == 0, N <= 2^24: the projection's output
  *   a_bf16       [adapters, R, K];  b_bf16 [adapters, N, R];  R % 8 == 0,

@@ -196,6 +196,35 @@ def test_lora_update_far_larger_than_the_projection():
     check_lora(3, 40, 512, 64, 16, [0, 40], [0], 1, by=1000.0)
 
 
+@pytest.mark.parametrize("M,K,N,R", [(40, 256, 80, 16), (70, 128, 48, 128), (33000, 128, 80, 16), (1100, 4096, 176, 72)])
+def test_lora_infinite_weights(M, K, N, R):
+    """An infinite element of B makes its column infinite, with the sign of its product with t, whether t
+    is one bf16 number (then the rest of it is 0) or not, and an infinite sum of both signs is NaN; a
+    NaN in x is its row's alone.  In tiles of 16 rows and of 128."""
+    x, y = randn(0, M, K), randn(1, M, N)
+    a, b = randn(2, 1, R, K, by=1 / math.sqrt(K)), randn(3, 1, N, R)
+    x[: M // 2] = 0.0
+    x[: M // 2, 5] = 2.0      # t = 2 A[:, 5]: bf16 numbers
+    a[0, :3, 5] = torch.tensor([0.5, -0.25, 0.75])
+    b[0, 3, 0], b[0, 7, 1], b[0, N - 1, 2] = float("inf"), float("inf"), -float("inf")
+    b[0, 20, 0], b[0, 20, 1] = float("inf"), float("inf")
+    b[0, 30, 4] = float("nan")
+    x[M - 2, 9] = float("nan")
+    st = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    with np.errstate(invalid="ignore"):
+        want, size = O.lora_add(f64(y), f64(x), f64(a), f64(b), [0, M], [0])
+    got = qs.lora_add(y, x, a, b, st, torch.zeros(1, dtype=torch.int32, device="cuda"), out=torch.empty_like(y))
+    nan = np.isnan(want)
+    assert nan[M - 2].all() and nan[:, 30].all() and nan[: M // 2, 20].all() and nan.sum() < M * N // 4
+    assert np.array_equal(np.isnan(f64(got)), nan)
+    inf = np.isinf(want)
+    assert inf[: M // 2, [3, 7, N - 1]].all() and (want[: M // 2, 7] < 0).all()
+    assert np.array_equal(f64(got)[inf], want[inf])
+    fin = ~(nan | inf)
+    tol = half(BF16) * np.abs(want) + (2 * U * (K + R + 8) + 2.0 ** -17) * size
+    assert (np.abs(f64(got)[fin] - want[fin]) <= tol[fin]).all()
+
+
 def test_lora_many_requests():
     """More requests than a block has threads; most rows in small tiles, empty ones between."""
     rng = np.random.default_rng(0)
