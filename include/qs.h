@@ -604,8 +604,9 @@ QS_API qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_str
  *   scale        [adapters] float, or NULL (1)
  *   seg_start    [requests + 1] int32 (device), ascending, within [0, M];
  *   seg_adapter  [requests] int32 (device), -1 .. adapters - 1.  A request
- *                whose rows or adapter are out of range is left out and makes
- *                qs_device_error report QS_ERR_RANGE.
+ *                whose rows or adapter are out of range (or whose end lies
+ *                before its start) is left out and makes qs_device_error report
+ *                QS_ERR_RANGE; requests behind it may be left out too.
  *   workspace    qs_lora_workspace_bytes(M, K, R, requests) bytes of device
  *                scratch, 16-byte aligned (-1 for rejected arguments)
  *   out_bf16     [M, N]; may be y_bf16 itself, else it and the workspace must

@@ -268,6 +268,21 @@ def test_lora_bad_requests_are_left_out():
     close(out, want, half(BF16) * np.abs(want) + (2 * U * 144 + 2.0 ** -17) * size, "lora")
 
 
+@pytest.mark.parametrize("starts,ids", [([1000, 1010, 1011], [0, 1]), ([0, 8, 4000, 4001], [0, 1, 1]), ([32, 32, 30], [0, 1]),
+                                        ([-400, -300], [0]), ([0, 0, 0], [0, 9]), ([0] * 400 + [2 ** 31 - 1], [0] * 400)])
+def test_lora_every_bad_request_is_reported(starts, ids):
+    """Requests whose rows no tile comes to, empty ones without an adapter, the last of many."""
+    x, y = randn(0, 32, 128), randn(1, 32, 32)
+    a, b = randn(2, 2, 8, 128), randn(3, 2, 32, 8)
+    ints = lambda t: torch.tensor(t, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full_like(y, -3.0)
+    qs.lora_add(y, x, a, b, ints(starts), ints(ids), out=out)
+    assert qs.qs_device_error() == 5
+    assert (out[8:] == -3).all()
+    qs.lora_add(y, x, a, b, ints([0, 8, 8, 32]), ints([0, -1, 1]), out=out)
+    assert qs.qs_device_error() == 0
+
+
 # ----------------------------------------------------------------------------------- select
 
 @pytest.mark.parametrize("dtype,D", [(BF16, 128), (F16, 128), (BF16, 64), (F16, 64)])
