@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "qs.h"
@@ -23,6 +24,7 @@
 #include "qs_sd4.cuh"
 #include "qs_sd4_mx.cuh"
 #include "qs_select.cuh"
+#include "qs_views.cuh"
 
 namespace {
 
@@ -250,6 +252,32 @@ qs_status launch_sd4_quant_tc(const void* x, int64_t rows, int64_t K, void* out,
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// A view may not reach further than this, in elements (what lies below overflows no offset).
+constexpr int64_t kMaxReach = 1LL << 46;
+
+bool reaches_too_far(int64_t size, int64_t stride) {
+  return size > 1 && stride > kMaxReach / (size - 1);
+}
+
+// The product, or a number beyond any memory.
+int64_t bytes_of(std::initializer_list<int64_t> sizes) {
+  int64_t n = 1;
+  for (const int64_t s : sizes)
+    if (__builtin_mul_overflow(n, s, &n) || n > (1LL << 56)) return 1LL << 56;
+  return n;
+}
+
+using qs::views::flat;
+using qs::views::View;
+
+// An output that lies apart from itself and from the other arguments (NULL ones aside).
+qs_status check_apart(const View& out, std::initializer_list<View> others) {
+  if (qs::views::overlaps_itself(out)) return QS_ERR_OVERLAP;
+  for (const View& v : others)
+    if (v.p && qs::views::overlap(out, v)) return QS_ERR_OVERLAP;
+  return QS_OK;
+}
+
 // A [B, L, H, D] view of 16-bit elements that 16-byte accesses and tensor maps can take.
 qs_status check_view(const void* p, const qs_strides* st, int64_t B, int64_t L, int64_t H,
                      int64_t D, int dtype) {
@@ -262,10 +290,14 @@ qs_status check_view(const void* p, const qs_strides* st, int64_t B, int64_t L, 
   for (int i = 0; i < 3; ++i) {
     if (size[i] == 1) continue;
     if (stride[i] < 0 || (i == 1 && stride[i] == 0)) return QS_ERR_SHAPE;
-    if (stride[i] >= (1LL << 39)) return QS_ERR_RANGE;
+    if (stride[i] >= (1LL << 39) || reaches_too_far(size[i], stride[i])) return QS_ERR_RANGE;
     if (stride[i] % 8 != 0) return QS_ERR_ALIGN;
   }
-  return check_device_ptr(p);
+  return QS_OK;
+}
+
+View view_of(const void* p, const qs_strides* st, int64_t B, int64_t L, int64_t H, int64_t D) {
+  return {p, 2 * D, {{B, B > 1 ? 2 * st->batch : 0}, {L, L > 1 ? 2 * st->row : 0}, {H, H > 1 ? 2 * st->head : 0}}};
 }
 
 qs_status check_ints(const int32_t* p) {
@@ -920,8 +952,20 @@ qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_stride, in
     return QS_ERR_SHAPE;
   const uintptr_t elem = dtype == QS_F32 ? 4 : 2;
   if (!aligned_to(x, elem) || !aligned_to(y, elem) || !aligned_to(positions, 8) ||
-      !aligned_to(inv_freq, 8))
+      !aligned_to(inv_freq, 8) || (pair_axis && !aligned_to(pair_axis, 4)))
     return QS_ERR_ALIGN;
+  for (const int64_t stride : {x_row_stride, y_row_stride})
+    if (reaches_too_far(rows, stride)) return QS_ERR_RANGE;
+  for (const int64_t stride : {x_head_stride, y_head_stride})
+    if (reaches_too_far(heads, stride)) return QS_ERR_RANGE;
+  const auto view = [&](const void* p, int64_t row, int64_t head) {
+    const int64_t n = static_cast<int64_t>(elem);
+    return View{p, head_dim * n, {{rows, rows > 1 ? row * n : 0}, {heads, heads > 1 ? head * n : 0}, {1, 0}}};
+  };
+  const View vx = view(x, x_row_stride, x_head_stride), vy = view(y, y_row_stride, y_head_stride);
+  QS_TRY(check_apart(vy, {flat(positions, bytes_of({rows, axes, 8})), flat(pair_axis, 2 * rot_dim),
+                          flat(inv_freq, 4 * rot_dim)}));
+  if (!qs::views::same(vx, vy)) QS_TRY(check_apart(vy, {vx}));
   QS_TRY(check_ints(pair_axis));
   QS_TRY(check_device_ptr(x));
   QS_TRY(check_device_ptr(y));
@@ -974,6 +1018,17 @@ qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t
   for (const void* p : tensors)
     if (!aligned16(p)) return QS_ERR_ALIGN;
   if (scale && !aligned_to(scale, 4)) return QS_ERR_ALIGN;
+  if (!aligned_to(seg_start, 4) || !aligned_to(seg_adapter, 4)) return QS_ERR_ALIGN;
+  const View out = flat(out_bf16, bytes_of({M, N, 2})), y = flat(y_bf16, bytes_of({M, N, 2})),
+             ws = flat(workspace, need);
+  const std::initializer_list<View> inputs = {
+      flat(x_bf16, bytes_of({M, K, 2})),      flat(a_bf16, bytes_of({adapters, R, K, 2})),
+      flat(b_bf16, bytes_of({adapters, N, R, 2})), flat(scale, 4 * adapters),
+      flat(seg_start, 4 * (requests + 1)),    flat(seg_adapter, 4 * requests)};
+  QS_TRY(check_apart(out, inputs));
+  QS_TRY(check_apart(ws, inputs));
+  QS_TRY(check_apart(ws, {out, y}));
+  if (out_bf16 != y_bf16) QS_TRY(check_apart(out, {y}));
   for (const void* p : tensors) QS_TRY(check_device_ptr(p));
   if (scale) QS_TRY(check_device_ptr(scale));
   QS_TRY(check_ints(seg_start));
@@ -999,8 +1054,11 @@ qs_status qs_block_means(const void* x, const qs_strides* x_strides, int64_t B, 
   const int64_t blocks = (L + QS_BLOCK_K - 1) / QS_BLOCK_K;
   if (first_block < 0 || first_block >= blocks) return QS_ERR_RANGE;
   if (B * H * blocks > QS_MAX_ROWS) return QS_ERR_RANGE;
-  if (!aligned16(means)) return QS_ERR_ALIGN;
+  if (!aligned16(means) || (len && !aligned_to(len, 4))) return QS_ERR_ALIGN;
+  QS_TRY(check_apart(flat(means, bytes_of({B, H, blocks, D, 4})),
+                     {view_of(x, x_strides, B, L, H, D), flat(len, 4 * B)}));
   QS_TRY(check_ints(len));
+  QS_TRY(check_device_ptr(x));
   QS_TRY(check_device_ptr(means));
   qs::select::MeanArgs a{};
   a.x = static_cast<const uint16_t*>(x), a.st = select_strides(x_strides), a.len = len;
@@ -1039,10 +1097,22 @@ qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B,
     if (!workspace) return QS_ERR_NULL;
     if (workspace_bytes < need || need / (D * 4) > QS_MAX_ROWS) return QS_ERR_RANGE;
     if (!aligned16(workspace)) return QS_ERR_ALIGN;
+  }
+  if ((q_len && !aligned_to(q_len, 4)) || (k_len && !aligned_to(k_len, 4))) return QS_ERR_ALIGN;
+  const View ws = flat(need > 0 ? workspace : nullptr, need);
+  const std::initializer_list<View> inputs = {
+      view_of(q, q_strides, B, Lq, Hq, D), flat(means, bytes_of({B, Hkv, nk, D, 4})),
+      flat(q_len, 4 * B), flat(k_len, 4 * B)};
+  const View lists = flat(blocks, bytes_of({B, Hq, (Lq + QS_BLOCK_Q - 1) / QS_BLOCK_Q, T, 4}));
+  QS_TRY(check_apart(lists, inputs));
+  QS_TRY(check_apart(lists, {ws}));
+  if (ws.p) {
+    QS_TRY(check_apart(ws, inputs));
     QS_TRY(check_device_ptr(workspace));
   }
   QS_TRY(check_ints(q_len));
   QS_TRY(check_ints(k_len));
+  QS_TRY(check_device_ptr(q));
   QS_TRY(check_device_ptr(means));
   QS_TRY(check_device_ptr(blocks));
   qs::select::SelectArgs a{};
@@ -1054,12 +1124,12 @@ qs_status qs_block_select(const void* q, const qs_strides* q_strides, int64_t B,
   a.first = static_cast<int>(keep_first < nk ? keep_first : nk);
   a.last = static_cast<int>(keep_last < nk ? keep_last : nk);
   a.causal = (flags & QS_ATTN_CAUSAL) != 0;
-  float* ws = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  float* q_means = need > 0 ? static_cast<float*>(workspace) : nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f16 = dtype == QS_F16;
   const cudaError_t e =
-      D == 64 ? (f16 ? qs::select::launch_select<64, true>(a, ws, s) : qs::select::launch_select<64, false>(a, ws, s))
-              : (f16 ? qs::select::launch_select<128, true>(a, ws, s) : qs::select::launch_select<128, false>(a, ws, s));
+      D == 64 ? (f16 ? qs::select::launch_select<64, true>(a, q_means, s) : qs::select::launch_select<64, false>(a, q_means, s))
+              : (f16 ? qs::select::launch_select<128, true>(a, q_means, s) : qs::select::launch_select<128, false>(a, q_means, s));
   return e == cudaSuccess ? QS_OK : QS_ERR_CUDA;
 }
 
@@ -1095,18 +1165,32 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
     if (!workspace) return QS_ERR_NULL;
     if (workspace_bytes < need) return QS_ERR_RANGE;
     if (!aligned16(workspace)) return QS_ERR_ALIGN;
-    QS_TRY(check_device_ptr(workspace));
   }
   const qs::attn::Plan p = qs::attn::plan(B, Hq, Lq, T);
   const int64_t nq = (Lq + QS_BLOCK_Q - 1) / QS_BLOCK_Q;
   if (B * Hq * nq * p.splits > INT32_MAX || B * Hq * Lq / 8 > INT32_MAX - 1) return QS_ERR_RANGE;
+  for (const void* ints : {static_cast<const void*>(blocks), static_cast<const void*>(q_len),
+                           static_cast<const void*>(k_len), static_cast<const void*>(lse)})
+    if (ints && !aligned_to(ints, 4)) return QS_ERR_ALIGN;
+  const View vo = view_of(out, out_strides, B, Lq, Hq, D), vl = flat(lse, bytes_of({B, Hq, Lq, 4})),
+             ws = flat(need > 0 ? workspace : nullptr, need);
+  const std::initializer_list<View> inputs = {
+      view_of(q, q_strides, B, Lq, Hq, D),  view_of(k, k_strides, B, Lk, Hkv, D),
+      view_of(v, v_strides, B, Lk, Hkv, D), flat(blocks, bytes_of({B, Hq, nq, T, 4})),
+      flat(q_len, 4 * B),                   flat(k_len, 4 * B)};
+  QS_TRY(check_apart(vo, inputs));
+  QS_TRY(check_apart(vo, {vl, ws}));
+  if (lse) QS_TRY(check_apart(vl, inputs));
+  if (ws.p) {
+    QS_TRY(check_apart(ws, inputs));
+    QS_TRY(check_apart(ws, {vl}));
+    QS_TRY(check_device_ptr(workspace));
+  }
+  for (const void* tensor : {q, k, v, static_cast<const void*>(out)}) QS_TRY(check_device_ptr(tensor));
   QS_TRY(check_ints(blocks));
   QS_TRY(check_ints(q_len));
   QS_TRY(check_ints(k_len));
-  if (lse) {
-    if (!aligned_to(lse, 4)) return QS_ERR_ALIGN;
-    QS_TRY(check_device_ptr(lse));
-  }
+  if (lse) QS_TRY(check_device_ptr(lse));
   const int sms = qs::sm_count();
   if (sms <= 0) return QS_ERR_CUDA;
   CUtensorMap mq, mk, mv, mo;
@@ -1182,6 +1266,7 @@ const char* qs_status_str(int status) {
     case QS_ERR_CUDA: return "CUDA call or launch failed";
     case QS_ERR_TIMEOUT: return "a kernel wait exceeded its bound";
     case QS_ERR_PTR: return "pointer is not device memory of the current device";
+    case QS_ERR_OVERLAP: return "an output shares memory with itself or with another argument";
     case QS_ERR_DTYPE: return "element type not taken by this operator";
     default: return "unknown status";
   }

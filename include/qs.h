@@ -66,7 +66,9 @@ typedef enum {
   QS_ERR_CUDA = 6,     /* a CUDA runtime/driver call or a launch failed */
   QS_ERR_TIMEOUT = 7,  /* a kernel wait exceeded its bound (reported by qs_device_error) */
   QS_ERR_PTR = 8,      /* a pointer is not device memory of the current device */
-  QS_ERR_DTYPE = 9     /* an element type that the operator does not take */
+  QS_ERR_DTYPE = 9,    /* an element type that the operator does not take */
+  QS_ERR_OVERLAP = 10  /* rows or heads of an output share memory, or an output (or the
+                          workspace) shares it with another argument */
 } qs_status;
 
 /* Test-only flag: skip the Hadamard rotation (the codes are then taken from the
@@ -545,7 +547,11 @@ QS_API qs_status qs_gelu_bf16(const void* x_bf16, int64_t n, void* y_bf16, void*
  * definitions here are this library's.  All are forward (serving) operators.
  *
  * Rotary positions, means, selection and attention take views: strides are in
- * ELEMENTS, the last dimension is contiguous.
+ * ELEMENTS, the last dimension is contiguous.  Outputs and workspaces lie apart
+ * from themselves (no two rows or heads share an element) and from the other
+ * arguments, but for the in-place forms named below; others are refused with
+ * QS_ERR_OVERLAP.  Views of one buffer between whose strides no order can be
+ * made out may be refused as well.
  */
 typedef enum { QS_BF16 = 0, QS_F16 = 1, QS_F32 = 2 } qs_dtype;
 
@@ -609,8 +615,7 @@ QS_API qs_status qs_rope(const void* x, int64_t x_row_stride, int64_t x_head_str
  *                QS_ERR_RANGE; requests behind it may be left out too.
  *   workspace    qs_lora_workspace_bytes(M, K, R, requests) bytes of device
  *                scratch, 16-byte aligned (-1 for rejected arguments)
- *   out_bf16     [M, N]; may be y_bf16 itself, else it and the workspace must
- *                not overlap the other arguments
+ *   out_bf16     [M, N]; may be y_bf16 itself
  */
 QS_API int64_t qs_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t requests);
 QS_API qs_status qs_lora_add(const void* x_bf16, const void* y_bf16, int64_t M, int64_t K,
@@ -685,7 +690,7 @@ QS_API qs_status qs_block_select(const void* q, const qs_strides* q_strides, int
  *   workspace qs_block_attention_workspace_bytes(B, Lq, Hq, D, T) bytes of
  *             device scratch, 16-byte aligned (0: none is needed and it may be
  *             NULL; -1 for rejected arguments)
- *   out       [B, Lq, Hq, D] view like q; must not overlap the inputs
+ *   out       [B, Lq, Hq, D] view like q
  *   lse       [B, Hq, Lq] float, the log of each row's softmax denominator,
  *             or NULL
  * Rows of out and lse at and behind q_len are left as they were.
