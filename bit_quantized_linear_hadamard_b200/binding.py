@@ -169,9 +169,14 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# torch.cuda.current_stream(device).cuda_stream without the objects around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream):
-    if stream is None:  # torch.cuda.current_stream().cuda_stream, without the objects around it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        device = torch.cuda.current_device()  # initialises CUDA, or says why it cannot
+        return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
