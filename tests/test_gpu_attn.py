@@ -138,6 +138,21 @@ def test_rope_any_alignment_and_order(dtype, offset, row):
     assert (guard[:, :, 0] == -7).all() and (guard[:, :, 129] == -7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("rows,heads,dim,rot", [(1301, 5, 128, 128), (1301, 3, 64, 48), (2400, 2, 128, 48), (1211, 7, 44, 30),
+                                                (1200, 1, 6, 6)])
+def test_rope_more_rows_than_processors(dtype, inter, rows, heads, dim, rot):
+    """Blocks of several rows, the last one not full; all heads of a row in one block."""
+    x = randn(rows, rows, heads + 2, dim, dtype=dtype, by=3.0)[:, 1:-1]
+    inv, axis, _ = qs.rope_frequencies(rot, axes=(rot - 4, 2, 2))
+    pos = torch.randint(0, 10 ** 6, (rows, 3), generator=torch.Generator().manual_seed(rot)).cuda()
+    got = check_rope(x, pos, inv, axis, inter, 1.25)
+    same = x.clone()
+    qs.rope(same, pos, inv, axis, inter, 1.25, out=same)
+    assert torch.equal(same, got)
+
+
 def test_rope_bad_axis_is_reported():
     x = randn(1, 2, 1, 8)
     inv, _, _ = qs.rope_frequencies(8)
@@ -190,6 +205,17 @@ def test_lora_long_requests(R, M, K):
     starts = [1, 2, M // 3 + 5, M // 3 + 5, M - 130, M - 2] if R > 32 else [1, M // 3 + 5, M - 130, M - 2]
     ids = [1, 0, 1, 2, -1] if R > 32 else [2, 0, -1]
     check_lora(50 + R, M, K, 80, R, starts, ids, 3, in_place=R % 16 == 0)
+
+
+@pytest.mark.parametrize("R", [16, 64, 72, 128])
+@pytest.mark.parametrize("M,K,N,starts", [
+    (4200, 1024, 4112, [3, 700, 701, 1900, 4150]),                       # many column chunks for each tile
+    (2200, 2048, 1040, [0, *range(1, 64), 2100]),                        # single tokens and one long prompt
+    (300, 512, 15376, [0, 5, 100, 300])])                                # few rows, many columns
+def test_lora_many_columns(R, M, K, N, starts):
+    """The stages, both accumulators and the column ranges serve one chunk after another."""
+    ids = [(3 * i) % 4 - 1 for i in range(len(starts) - 2)] + [1]
+    check_lora(R, M, K, N, R, starts, ids, 3, in_place=R == 64)
 
 
 def test_lora_update_far_larger_than_the_projection():
@@ -348,6 +374,19 @@ def test_block_select_ties_and_special_scores():
 def test_block_select_many_blocks():
     """Rows of scores that leave room for one query block per CTA."""
     check_select(8, 1, 260, 24000 * 64, 1, 1, 64, 40)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,D,B,Lq,Lk,Hq,Hkv,T,ragged", [(BF16, 128, 1, 16645, 640, 8, 2, 4, False),
+                                                              (F16, 64, 2, 9000, 9000, 8, 1, 23, True)])
+def test_block_select_more_query_blocks_than_are_formed_on_the_way(causal, dtype, D, B, Lq, Lk, Hq, Hkv, T, ragged):
+    """Above 1024 query blocks in all their means have a kernel of their own and a workspace."""
+    ql, kl = ([torch.tensor(n, dtype=torch.int32, device="cuda") for n in ([Lq, 7001], [Lk, 8200])] if ragged else (None, None))
+    assert qs.qs_block_select_workspace_bytes(B, Lq, Hq, D) > 0
+    q = randn(1, B, Lq, Hq, D, dtype=dtype)
+    if ragged:
+        q[1, 7001:] = float("nan")
+    check_select(1, B, Lq, Lk, Hq, Hkv, D, T, q=q, causal=causal, first=1, last=1, q_len=ql, k_len=kl)
 
 
 # -------------------------------------------------------------------------------- attention
