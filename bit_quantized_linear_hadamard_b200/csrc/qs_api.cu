@@ -1203,7 +1203,11 @@ qs_status qs_block_attention(const void* q, const qs_strides* q_strides, const v
       !qs::attn::make_map(&mo, out, D, Lq, Hq, B, out_strides->row, out_strides->head,
                           out_strides->batch, QS_BLOCK_Q))
     return QS_ERR_CUDA;
+  const auto operand = [](const void* t, const qs_strides* st) {
+    return qs::attn::View{static_cast<const uint16_t*>(t), st->batch, st->row, st->head};
+  };
   qs::attn::Args a{};
+  a.q = operand(q, q_strides), a.k = operand(k, k_strides), a.v = operand(v, v_strides);
   a.out = out, a.o_batch = out_strides->batch, a.o_row = out_strides->row;
   a.o_head = out_strides->head, a.lse = lse, a.blocks = blocks;
   a.q_len = q_len, a.k_len = k_len, a.part = static_cast<float*>(workspace);

@@ -77,7 +77,7 @@ struct Cfg {
   static constexpr int kItemFull = kOFree + 1, kItemEmpty = kItemFull + kItemRing;
   static constexpr int kDrain = kItemEmpty + kItemRing, kNumBars = kDrain + 2;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 32 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   __device__ static int arrivals(int i) {
     const auto in = [&](int first, int n) { return i >= first && i < first + n; };
@@ -91,7 +91,13 @@ struct Cfg {
   }
 };
 
+struct View {
+  const uint16_t* p;
+  int64_t batch, row, head;  // strides in elements
+};
+
 struct Args {
+  View q, k, v;  // as the tensor maps have them
   void* out;
   int64_t o_batch, o_row, o_head;  // strides in elements
   float* lse;                      // [B, Hq, Lq] or NULL
@@ -311,11 +317,114 @@ __device__ __forceinline__ Item item_at(const Args& a, unsigned i) {
   return it;
 }
 
+// The largest, or NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Rows whose output has a NaN although their sum is finite, formed again from the keys that they see
+// alone, in binary32: in the matrix products a key that a row does not see has P = 0, and 0 times an
+// infinity or a NaN of that key's v is a NaN.  The block's four groups of 128 threads go through its
+// items once more, a row and 64 columns to a thread.  Only blocks that met such a row come here.  In
+// the loop over the items this code cost 2 to 9 %, here 1 to 3 % where items are short (causal, 2 x
+// 4099 rows, 32 / 8 heads, D 128: 197.8 -> 200.4 us) and nothing where they are long.
+template <int D, bool F16>
+__device__ __noinline__ void rows_again(const Args& a, unsigned items) {
+  const int half = threadIdx.x / kBQ, r = threadIdx.x % kBQ;
+  if (half >= D / 64) return;
+  const int64_t nk = (a.Lk + kBK - 1) / kBK, parts = static_cast<int64_t>(a.B) * a.Hq * a.Lq;
+  const float scale2 = a.scale * kLog2e;
+  float o[64];
+  for (unsigned i = blockIdx.x; i < items; i += gridDim.x) {
+    const Item it = item_at(a, i);
+    const int row = it.row0 + r, off = it.kl - it.ql, limit = min(it.kl, row + off + 1);
+    if (row >= it.ql || limit >= min(it.kl, it.row0 + kBQ + off)) continue;
+    const int64_t flat = (static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Lq + row;
+    float4* part = reinterpret_cast<float4*>(a.part + (it.split * parts + flat) * D + 64 * half);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + it.b * a.o_batch + row * a.o_row +
+                                          it.h * a.o_head + 64 * half);
+    bool nan = false;
+    for (int k = 0; k < 16; ++k) {
+      if (a.splits > 1) {
+        const float4 v = part[k];
+        nan |= isnan(v.x) || isnan(v.y) || isnan(v.z) || isnan(v.w);
+      } else {
+        const uint2 v = reinterpret_cast<const uint2*>(out)[k];
+        const float2 x = unpack2<F16>(v.x), y = unpack2<F16>(v.y);
+        nan |= isnan(x.x) || isnan(x.y) || isnan(y.x) || isnan(y.y);
+      }
+    }
+    if (!nan) continue;
+    const int hk = it.h / (a.Hq / a.Hkv);
+    const uint4* q = reinterpret_cast<const uint4*>(a.q.p + it.b * a.q.batch + row * a.q.row + it.h * a.q.head);
+    const int32_t* list = a.blocks + ((static_cast<int64_t>(it.b) * a.Hq + it.h) * a.nq + it.row0 / kBQ) * a.T +
+                          static_cast<int64_t>(it.split) * a.chunk;
+    const int len = min(a.chunk, a.T - it.split * a.chunk);
+    float m = -INFINITY, l = 0.f;
+    bool some = true;  // columns that are not NaN yet
+    for (int e = 0; e < 64; ++e) o[e] = 0.f;
+    for (int n = 0; n < 64 * len && some; ++n) {
+      const int entry = list[n / 64], j = entry * kBK + n % 64;
+      if (entry < 0 || entry >= nk || j >= limit) continue;
+      const uint4* k = reinterpret_cast<const uint4*>(a.k.p + it.b * a.k.batch + j * a.k.row + hk * a.k.head);
+      float s = 0.f;
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = q[c], y = k[c];
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 u = unpack2<F16>(xw[w]), t = unpack2<F16>(yw[w]);
+          s = fmaf(u.x, t.x, fmaf(u.y, t.y, s));
+        }
+      }
+      s *= scale2;
+      if (s == -INFINITY) continue;  // p = 0
+      if (s > m) {
+        const float f = exp2f(m - s);
+        for (int e = 0; e < 64; ++e) o[e] *= f;
+        l *= f, m = s;
+      }
+      const float p = exp2f(s - m);
+      l += p;
+      const uint4* v =
+          reinterpret_cast<const uint4*>(a.v.p + it.b * a.v.batch + j * a.v.row + hk * a.v.head + 64 * half);
+      some = false;
+      for (int c = 0; c < 8; ++c) {
+        const uint4 y = v[c];
+        const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+        for (int w = 0; w < 4; ++w) {
+          const float2 t = unpack2<F16>(yw[w]);
+          float &x0 = o[8 * c + 2 * w], &x1 = o[8 * c + 2 * w + 1];
+          x0 = fmaf(p, t.x, x0), x1 = fmaf(p, t.y, x1);
+          some |= !isnan(x0) || !isnan(x1);
+        }
+      }
+    }
+    if (!some || !(l > 0.f)) continue;  // NaN throughout: as it is
+    const float inv = 1.f / l;
+    for (int e = 0; e < 64; e += 4) {
+      const float4 v = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+      if (a.splits > 1)
+        part[e / 4] = v;
+      else
+        reinterpret_cast<uint2*>(out)[e / 4] = make_uint2(pack2<F16>(v.x, v.y), pack2<F16>(v.z, v.w));
+    }
+  }
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                const Args a) {
+                const __grid_constant__ Args a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -329,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + C::kOffMisc + 4);
   int* staged_warps = reinterpret_cast<int*>(sp + C::kOffMisc + 8);  // per 64 columns, modulo 4
+  volatile int* rows_left = reinterpret_cast<volatile int*>(sp + C::kOffMisc + 16);  // for rows_again
   const auto bar = [&](int i) { return sbase + C::kOffBar + 8u * i; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -338,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kNumBars; ++i) mbar_init(bar(i), C::arrivals(i));
     *abort_flag = 0;
     staged_warps[0] = staged_warps[1] = 0;
+    *rows_left = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -556,6 +667,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto value = [&](int k) {
           return inv == 0.f ? 0.f : __uint_as_float(o[k / 32][k % 32]) * inv;
         };
+        // a finite sum beside a NaN: of a key that only other rows of the block see, or one that this does
+        if (a.causal && write && inv > 0.f && limit < min(it.kl, it.row0 + kBQ + off)) {
+          float most = 0.f;
+#pragma unroll
+          for (int k = 0; k < 64; k += 2)
+            most = max3_nan(most, __uint_as_float(o[k / 32][k % 32]), __uint_as_float(o[k / 32][k % 32 + 1]));
+          if (isnan(most)) *rows_left = 1;
+        }
         if (a.splits > 1) {
           if (write) {
             float4* part = reinterpret_cast<float4*>(a.part + (it.split * parts + flat) * D + 64 * half);
@@ -834,6 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (*rows_left) rows_again<D, F16>(a, items);
 }
 
 // Joins the parts of each row, in the order of the splits: a warp takes a row.  (Four parts at a

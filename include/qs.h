@@ -680,8 +680,7 @@ QS_API qs_status qs_block_select(const void* q, const qs_strides* q_strides, int
  *   q, k, v   [B, Lq, Hq, D], [B, Lk, Hkv, D] x 2 views, QS_BF16 or QS_F16, D 64
  *             or 128, 16-byte aligned, strides multiples of 8 elements below
  *             2^39 (a batch or head stride of 0 shares one tensor).  A
- *             non-finite value in a valid row of v reaches every row of the
- *             query blocks that list its block, causal or not.
+ *             non-finite value in v reaches the rows that see its key.
  *   blocks    [B, Hq, ceil(Lq / QS_BLOCK_Q), T] int32 in any order; -1 is no
  *             block, a block listed twice counts twice, and a value outside
  *             [-1, ceil(Lk / QS_BLOCK_K)) is left out and makes

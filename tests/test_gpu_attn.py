@@ -572,6 +572,36 @@ def test_attention_more_items_than_processors(monkeypatch, dtype, D, causal, B, 
         assert torch.equal(o, got) and torch.equal(z, lse)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F16, 64), (BF16, 64), (F16, 128)])
+@pytest.mark.parametrize("Lq,Lk,T", [(300, 300, 5), (300, 411, 7), (5, 900, 15), (64, 4096, 64)])
+def test_attention_values_of_keys_that_a_row_does_not_see(dtype, D, bad, Lq, Lk, T):
+    """Causal: a NaN or an infinity in v reaches the rows that see its key, and no other row of the
+    block; with lists that are cut too (5 and 64 queries)."""
+    q, k, v = randn(0, 2, Lq, 2, D, dtype=dtype), randn(1, 2, Lk, 1, D, dtype=dtype), randn(2, 2, Lk, 1, D, dtype=dtype)
+    off = Lk - Lq
+    for key in (off + 3, off + Lq // 2, Lk - 1):
+        v[0, key, 0, 7] = bad
+        v[1, key, 0] = bad
+    v[0, off + 2, 0, 9], v[0, off + 3, 0, 9] = float("inf"), -float("inf")
+    nq, nk = -(-Lq // 128), -(-Lk // 64)
+    blocks = np.tile(np.arange(nk, dtype=np.int32)[::-1][:T], (2, 2, nq, 1))
+    clean = torch.where(v.isfinite(), v, 0.0)
+    with np.errstate(invalid="ignore"):
+        want, wlse, _ = O.block_attention(f64(q), f64(k), f64(v), blocks, None, True)
+    got, lse = qs.block_attention(q, k, v, torch.tensor(blocks, device="cuda"), causal=True)
+    base, blse = check_attention(q, k, clean, blocks, causal=True)
+    bad = ~np.isfinite(want)
+    assert 0 < bad.sum() < bad.size
+    assert np.array_equal(f64(got)[bad], want[bad], equal_nan=True)
+    assert torch.equal(lse, blse)
+    # finite elements: as with those values 0, but summed apart from the products, and P not rounded
+    e = half(dtype)
+    size = O.block_attention(f64(q), f64(k), f64(clean), blocks, None, True)[2]
+    tol = 2 * (e * np.abs(f64(base)) + (e + 2.0 ** -12) * size) + Lk * 2.0 ** -23
+    assert (np.abs(f64(got)[~bad] - f64(base)[~bad]) <= tol[~bad]).all()
+
+
 def test_attention_at_once_on_two_streams():
     q, k, v = randn(0, 2, 300, 4, 128), randn(1, 2, 700, 2, 128), randn(2, 2, 700, 2, 128)
     blocks = torch.tensor(some_blocks(0, 2, 4, 300, 700, 7), device="cuda")
