@@ -37,10 +37,16 @@
 #include "qs.h"
 #include "qs_host.cuh"
 #include "qs_launch.cuh"
+#include "qs_ops.cuh"
 #include "qs_ptx.cuh"
 
 namespace qs {
 namespace attn {
+
+using ops::checked_len;
+using ops::idesc_f16;
+using ops::max3_nan;
+using ops::mma_ss;
 
 constexpr int kBQ = QS_BLOCK_Q, kBK = QS_BLOCK_K, kTileK = 2 * kBK;
 constexpr int kGroups = 3, kGroupWarps = 4;
@@ -113,26 +119,6 @@ struct Args {
   int q_by_head, q_by_batch, k_by_head, k_by_batch, v_by_head, v_by_batch;
 };
 
-// Instruction descriptor: kind::f16, binary32 D, A K-major, B K-major or MN-major.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool f16, bool b_mn) {
-  return (1u << 4)                                 // D format: F32
-         | ((f16 ? 0u : 1u) << 7)                  // A: F16 or BF16
-         | ((f16 ? 0u : 1u) << 10)                 // B: the same
-         | ((b_mn ? 1u : 0u) << 16)                // B: N contiguous
-         | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
-         | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
-}
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // A from tensor memory: row = lane, two consecutive k per 32-bit column.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -163,19 +149,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
-}
-
-// Whether the phase has completed, without the suspension of try_wait.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -244,17 +217,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A length given on the device, held to [0, most]; outside it the error word is raised.
-__device__ __forceinline__ int checked_len(const int32_t* len, int b, int64_t most) {
-  if (!len) return static_cast<int>(most);
-  const int n = len[b];
-  if (n < 0 || n > most) {
-    atomicOr(&g_error_word, kErrIndex);
-    return n < 0 ? 0 : static_cast<int>(most);
-  }
-  return n;
-}
-
 // The scores of a row go through registers 32 at a time, in rolled loops: unrolled over the tile,
 // the three groups' code did not stay in the instruction caches and waited for its fetches.
 
@@ -311,17 +273,10 @@ __device__ __forceinline__ Item item_at(const Args& a, unsigned i) {
   i /= static_cast<unsigned>(a.nq);
   it.h = static_cast<int>(i % static_cast<unsigned>(a.Hq));
   it.b = static_cast<int>(i / static_cast<unsigned>(a.Hq));
-  it.ql = checked_len(a.q_len, it.b, a.Lq);
-  it.kl = checked_len(a.k_len, it.b, a.Lk);
+  it.ql = static_cast<int>(checked_len(a.q_len, it.b, a.Lq));
+  it.kl = static_cast<int>(checked_len(a.k_len, it.b, a.Lk));
   it.tiles = 0;
   return it;
-}
-
-// The largest, or NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 template <bool F16>

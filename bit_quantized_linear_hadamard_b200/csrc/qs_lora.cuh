@@ -35,10 +35,14 @@
 #include "qs.h"
 #include "qs_host.cuh"
 #include "qs_launch.cuh"
+#include "qs_ops.cuh"
 #include "qs_ptx.cuh"
 
 namespace qs {
 namespace lora {
+
+using ops::max3_nan;
+using ops::mma_ss;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -126,13 +130,6 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The largest, or NaN if one of them is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) {
@@ -229,16 +226,6 @@ struct ShrinkCfg {
 };
 constexpr int kShrinkThreads = 32 * 6;
 
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 template <int RN>
 __global__ void __launch_bounds__(kShrinkThreads)
     shrink_large_kernel(const __grid_constant__ CUtensorMap tmX,
@@ -291,9 +278,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     for (int k = i > C::kStages ? i - C::kStages : 0; k < i; ++k)
       mbar_wait_limit(full(k % C::kStages), (k / C::kStages) & 1, kWaitTimeoutNs, kErrWaitTma);
   } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |  // binary32 D, bf16 A and B
-                               (static_cast<uint32_t>(RN >> 3) << 17) |
-                               (static_cast<uint32_t>(kLargeRows >> 4) << 24);
+    constexpr uint32_t idesc = ops::idesc_f16(kLargeRows, RN, false, false);
     for (int i = 0; i < n; ++i) {
       const int s = i % C::kStages;
       if (!mbar_wait_bounded(full(s), (i / C::kStages) & 1, abort_flag, kErrWaitTma)) break;
@@ -301,7 +286,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       const uint32_t x = sbase + s * C::kStage;
 #pragma unroll
       for (int k = 0; k < kStepK / 16; ++k)
-        mma_bf16_ss(tmem, smem_desc_sw128(x + 32 * k), smem_desc_sw128(x + C::kX + 32 * k), idesc,
+        mma_ss(tmem, smem_desc_sw128(x + 32 * k), smem_desc_sw128(x + C::kX + 32 * k), idesc,
                     i != 0 || k != 0);
       mma_commit(empty(s));
     }
@@ -527,9 +512,7 @@ __global__ void __launch_bounds__(kExpandThreads)
       mbar_wait_limit(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitTimeoutNs,
                       kErrWaitTma);
   } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |  // binary32 D, bf16 A and B
-                               (static_cast<uint32_t>(C::kCols >> 3) << 17) |
-                               (static_cast<uint32_t>(kLargeRows >> 4) << 24);
+    constexpr uint32_t idesc = ops::idesc_f16(kLargeRows, C::kCols, false, false);
     const int steps = (a.R + 15) / 16;
     wait(C::kTFull, 0, kErrWaitEpilogue);
     for (int i = 0; i < n && ok; ++i) {
@@ -541,7 +524,7 @@ __global__ void __launch_bounds__(kExpandThreads)
       const uint32_t b = sbase + C::kOffStage + s * C::kStage + C::kY;
       for (int part = 0; part < 2; ++part)  // tops, rest
         for (int k = 0; k < steps; ++k)
-          mma_bf16_ss(tmem + C::kCols * buf,
+          mma_ss(tmem + C::kCols * buf,
                       smem_desc_sw128(sbase + part * C::kT + (k / 4) * kLargeRows * 128 + (k % 4) * 32),
                       smem_desc_sw128(b + (k / 4) * C::kCols * 128 + (k % 4) * 32), idesc,
                       part != 0 || k != 0);

@@ -23,10 +23,12 @@
 #include <cstdint>
 
 #include "qs.h"
-#include "qs_ptx.cuh"
+#include "qs_ops.cuh"
 
 namespace qs {
 namespace select {
+
+using ops::checked_len;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -72,17 +74,6 @@ __device__ __forceinline__ double2 unpack(uint32_t w) {
     u = __uint_as_float(w << 16), v = __uint_as_float(w & 0xFFFF0000u);
   }
   return make_double2(u, v);
-}
-
-// A length given on the device, held to [0, most]; outside it the error word is raised.
-__device__ __forceinline__ int64_t checked_len(const int32_t* len, int b, int64_t most) {
-  if (!len) return most;
-  const int64_t n = len[b];
-  if (n < 0 || n > most) {
-    atomicOr(&g_error_word, kErrIndex);
-    return n < 0 ? 0 : most;
-  }
-  return n;
 }
 
 // A warp's sum of `rows` rows of D elements: D / 8 lanes take 16 bytes of a row each, the warp
