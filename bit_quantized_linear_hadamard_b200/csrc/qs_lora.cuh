@@ -86,7 +86,10 @@ inline Plan plan(int64_t M, int64_t K, int64_t R, int64_t requests) {
   int64_t n = 2 * kSms / blocks;
   const int64_t most = p.large ? K / (16 * kStepK) : K / 512;
   if (n > most) n = most;
-  if (p.large && n > 4) n = 4;  // the second kernel reads every slice of t once per column range
+  // The second kernel reads every slice of t once per column range.  1, 2, 4, 6, 8 slices, us: M 4099
+  // of nine requests, K 13824, R 32: 93, 67, 56, 56, 56; M 2048, K 13824, R 64: 85, 57, 43, 45, 46;
+  // M 512, R 128: 100, 70, 55, 66, 70.
+  if (p.large && n > 4) n = 4;
   p.slices = static_cast<int>(n < 1 ? 1 : n);
   return p;
 }
@@ -732,6 +735,42 @@ cudaError_t launch_shrink_large(const Args& a, const Plan& p, cudaStream_t strea
   return cudaGetLastError();
 }
 
+// A block's t in chunks of y, by bytes.
+inline int64_t t_chunks(const Args& a) {
+  return (static_cast<int64_t>(a.R) * a.slices * 4 + 127) / 128;
+}
+
+// Column chunks of a large tile's block.  A tile's last block may have fewer; the GPU takes the full
+// ones first.  The time of `slots` blocks at once is counted in chunks, a block's beginning and end as
+// two and two for each of its t's, for one to three rounds of blocks, and the shortest taken.
+// One, two, three, four rounds, us: R 64, M 32760, K 5120, N 13824: 426, 428, 423, 429; N 5120: 209,
+// 215, 221, 222; R 32, M 8192, N 15360: 112, 121, 133, 142; R 128, M 32760, N 13824: 620, 571, 634,
+// 621; R 48, M 20000, N 10240: 261, 223, 216, 228.  The choice is the best of these, or within 1.5 %.
+inline int64_t chunks_each(int64_t tiles, int64_t chunks, int64_t t, int64_t slots) {
+  const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  int64_t best = 0, least = 0;
+  for (int64_t rounds = 1; rounds <= 3; ++rounds) {
+    int64_t each = up(tiles * chunks, slots * rounds);
+    each = each > chunks ? chunks : each < t ? t : each;  // t is not to be more to read than y
+    const int64_t ranges = up(chunks, each), full = tiles * (ranges - 1), begin = 2 + 2 * t;
+    const int64_t cost_full = each + begin, cost_last = chunks - each * (ranges - 1) + begin;
+    const int64_t used = full % slots;
+    int64_t rest;  // the last, partly filled round of full blocks, and the tiles' last ones
+    if (used == 0) {
+      rest = up(tiles, slots) * cost_last;
+    } else {
+      // the last ones on the slots left free, or also on the others behind the full ones
+      const int64_t alone = up(tiles, slots - used) * cost_last;
+      const int64_t left = tiles - (slots - used) * (cost_full / cost_last);
+      const int64_t shared = cost_full + (left > 0 ? up(left, slots) * cost_last : 0);
+      rest = alone < cost_full ? cost_full : alone < shared ? alone : shared;
+    }
+    const int64_t cost = full / slots * cost_full + rest;
+    if (rounds == 1 || cost < least) best = each, least = cost;
+  }
+  return best;
+}
+
 template <int KH>
 cudaError_t launch_expand_large(const Args& a, const Plan& p, cudaStream_t stream) {
   using C = ExpandCfg<KH>;
@@ -744,13 +783,8 @@ cudaError_t launch_expand_large(const Args& a, const Plan& p, cudaStream_t strea
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  // one round of blocks, or more where a block would have over 27 chunks; a block's t should not
-  // be more to read than its y
   const int64_t chunks = (a.N + C::kCols - 1) / C::kCols;
-  const int64_t t_chunks = (static_cast<int64_t>(a.R) * a.slices * kLargeRows * 4 + C::kY - 1) / C::kY;
-  int64_t each = (p.tiles * chunks + 2 * kSms - 1) / (2 * kSms);
-  each = each > 27 ? 27 : each;
-  each = each < t_chunks ? t_chunks : each;
+  const int64_t each = chunks_each(p.tiles, chunks, t_chunks(a), (KH == 1 ? 2 : 1) * kSms);
   const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>((chunks + each - 1) / each));
   return launch_behind(kern, grid, kExpandThreads, C::kSmemBytes, stream, y, w, o, a,
                        static_cast<int>(each));
