@@ -82,7 +82,10 @@ inline Plan plan(int64_t M, int64_t K, int64_t R, int64_t requests) {
   const int rows = p.large ? kLargeRows : kSmallRows;
   p.tiles = M / rows + requests;
   const int64_t blocks = p.large ? p.tiles : p.tiles * ((R + kGroup - 1) / kGroup);
-  // about two blocks per SM; small tiles: 64 k and more for each warp, large ones: 16 stages
+  // About two blocks per SM; small tiles: 64 k and more for each warp, large ones: 16 stages.  Small
+  // tiles, 1, 2, 3, 4 blocks per SM, us: 256 rows of 64 requests, K and N 5120, R 32: 22.3, 16.3, 15.5,
+  // 18.1; 64 tokens, N 15360, R 64: 34.8, 32.1, 38.0, 35.4.  32, 64, 128, 256 k a warp: one token, R 16:
+  // 6.1, 5.7, 5.6, 7.0.
   int64_t n = 2 * kSms / blocks;
   const int64_t most = p.large ? K / (16 * kStepK) : K / 512;
   if (n > most) n = most;
@@ -792,10 +795,13 @@ cudaError_t launch_expand_large(const Args& a, const Plan& p, cudaStream_t strea
 
 template <int KS>
 cudaError_t launch_expand_small(const Args& a, const Plan& p, cudaStream_t stream) {
-  // a block's t costs as much as a few column groups: about five blocks per SM, up to eight groups
+  // A block's t costs as much as a few column groups: about two blocks per SM, up to sixteen groups.
+  // With 2, 5, 8 blocks per SM, us: 64 tokens, N 15360, R 16: 19.1, 20.1, 22.9; N 5120, R 128: 40.4,
+  // 59.6, 59.5; 512 rows, R 64: 21.7, 25.8, 30.2.  Up to 8, 16, 32 groups: M 8000 of 64 requests, N
+  // 8960, R 16: 104, 98, 98.
   const int64_t groups = (a.N + 32 * kWarps - 1) / (32 * kWarps);
-  int64_t each = p.tiles * groups / (5 * kSms);
-  each = each < 1 ? 1 : each > 8 ? 8 : each;
+  int64_t each = p.tiles * groups / (2 * kSms);
+  each = each < 1 ? 1 : each > 16 ? 16 : each;
   const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>((groups + each - 1) / each));
   return launch_behind(expand_small_kernel<KS>, grid, kThreads, 0, stream, a,
                        static_cast<int>(32 * kWarps * each));
