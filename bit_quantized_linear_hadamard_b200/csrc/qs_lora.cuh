@@ -70,15 +70,16 @@ struct Plan {
 
 inline Plan plan(int64_t M, int64_t K, int64_t R, int64_t requests) {
   Plan p;
-  // Large tiles cost a fixed time each and pay from full ones on; small ones form up to 64 ranks
-  // in registers and read y and B once for each 16 rows.  By rows per request (uneven lengths),
-  // large / small, us, M 8192, K and N 5120: R 16: 119 / 84 at 128, 88 / 84 at 1024; R 32: 118 /
-  // 95 at 128, 107 / 93 at 256 (K 13824: 129 / 137), 40 / 64 at M 4096 of one request; R 64:
-  // 247 / 219 at 16, 167 / 165 at 32, 122 / 155 at 128; R 128: 246 / 297 at 32.  Little x in all:
-  // 23 / 19 at M 512 R 32, 20 / 16 at M 1024 K 1536 R 48.
-  const int64_t rows_each = M / requests;
-  p.large = M * K >= (1 << 22) &&
-            (R > 32 ? rows_each >= kLargeRows / 4 : rows_each * R * R >= (1 << 18));
+  // Large tiles cost a fixed time each and pay from some rows per request on; small ones form up to 64
+  // ranks in registers and read y and B once for each 16 rows.  By rows per request (uneven lengths),
+  // large / small, us, M 8192, K and N 5120: R 16: 88 / 79 at 195, 80 / 79 at 256, 66 / 77 at 512; R 32:
+  // 133 / 109 at 64, 116 / 109 at 80, 102 / 109 at 96; R 48: 141 / 130 at 64, 121 / 129 at 80; R 64: 172 /
+  // 166 at 32, 142 / 163 at 48, 137 / 139 at 64; R 128: 386 / 351 at 24, 263 / 319 at 32.  M 3000, N
+  // 13824: R 64: 132 / 116 at 48; R 128: 272 / 233 at 28.  The rule sees the mean only.  One long request
+  // and 63 single tokens: 58 / 56 at M 2063 R 64, 113 / 116 at R 128, 65 / 99 at M 4000 R 64; 82 / 113 at M
+  // 8000 R 32.  Little x in all: 21 / 15 at M 512 R 32, 42 / 36 at R 128, 18 / 14 at M 1024 K 1536 R 48.
+  const int64_t least_rows = R <= 16 ? 256 : R <= 32 ? 96 : R <= 48 ? 72 : R <= 64 ? 56 : 32;
+  p.large = M * K >= (1 << 22) && M / requests >= least_rows;
   const int rows = p.large ? kLargeRows : kSmallRows;
   p.tiles = M / rows + requests;
   const int64_t blocks = p.large ? p.tiles : p.tiles * ((R + kGroup - 1) / kGroup);
