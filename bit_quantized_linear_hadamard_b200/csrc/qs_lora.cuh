@@ -5,8 +5,9 @@
 // Two kernels.  "Shrink" forms t in binary32 partial sums over slices of K (a workspace
 // [slices][M][R]; the second kernel adds the slices in order, so the result does not depend on
 // timing).  "Expand" multiplies t, scaled, with B and adds y.  Its products run on bf16 tensor
-// cores with t as the sum of two bf16 numbers (t to 2^-17, below a bf16 output's half step
-// whatever the ratio of the update to y), sums in binary32.
+// cores with t as the sum of two bf16 numbers: t to 2^-17, so the update is off by 2^-17 of the sum of
+// its terms' magnitudes (half a step of a bf16 output is 2^-9 to 2^-8 of it: where y and the update, or
+// its terms, cancel to less than 2^-8 of their size, the former counts).  Sums in binary32.
 //
 // Rows go in tiles of BM of one request.  Tile number t -> (request, row) without a prefix sum:
 // request s owns the tile numbers from start[s] / BM + s on; as ceil(len / BM) <= (start + len) /
