@@ -432,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kTmaWarp) {
     // ---- row groups.  A barrier of parity p is only ever waited on when its phase before the
-    // awaited one is known to be complete: S of tile g is formed when P V of tile g - 3 is done.
+    // awaited one is known to be complete: S of tile g is formed when P V of tile g - 3 is done (and
+    // so V of tile g - 3 was there; of g - 2 it need not be).
     const int group = warp / kGroupWarps, quarter = warp % kGroupWarps;
     const int r = threadIdx.x % kBQ;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
@@ -482,6 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.kl < a.Lk &&
             (tile.x + kBK > it.kl || (tile.y < it.kl && tile.y + kBK > it.kl))) {
           const int slot = static_cast<int>(g % C::kStages);
+          // The stage may still wait for, or hold, the V of the tile that had it before, which S of
+          // this tile says nothing about where there are fewer stages than groups.
+          if (C::kStages < kGroups && g >= C::kStages)
+            wait(C::kPvDone + (g - C::kStages) % kGroups, ((g - C::kStages) / kGroups) & 1,
+                 kErrWaitEpilogue);
           wait(C::kVFull + slot, (g / C::kStages) & 1, kErrWaitTma);
           const int key = r < kBK ? tile.x + r : tile.y + r - kBK;  // this thread's row of V
           if (ok && key >= it.kl)

@@ -572,6 +572,38 @@ def test_attention_more_items_than_processors(monkeypatch, dtype, D, causal, B, 
         assert torch.equal(o, got) and torch.equal(z, lse)
 
 
+@pytest.mark.parametrize("behind", [1.0, float("nan")])
+@pytest.mark.parametrize("dtype,D", [(F16, 128), (BF16, 128), (BF16, 64)])
+@pytest.mark.parametrize("kl", [[558, 20, 500, 97], [1279, 558, 64, 321]])
+def test_attention_values_behind_a_length_beside_tiles_before_them(monkeypatch, dtype, D, behind, kl):
+    """Rows of V behind a length become 0 in the tile that holds them and in no tile that had its place in
+    shared memory before, however late that tile's V comes: the same to the last bit in every run.  The
+    batch is 12 times the same sequences, of several items per CTA."""
+    copies, H, Lk, T = 12, 4, 1280, 15
+    again = lambda t: t.repeat(copies, 1, 1, 1)  # noqa: E731
+    q, k, v = (randn(i, 4, Lk, H if i == 0 else 1, D, dtype=dtype) for i in range(3))
+    clean = tuple(again(t.clone()) for t in (q, k, v))
+    for b, n in enumerate(kl):
+        k[b, n:], v[b, n:] = behind, behind
+    seen = [-(-n // 64) for n in kl]
+    blocks = np.full((4, H, 10, T), -1, dtype=np.int32)
+    for b in range(4):
+        blocks[b, ..., : min(T, seen[b])] = np.arange(max(0, seen[b] - T), seen[b])
+    real = O.block_attention
+
+    def once(q, k, v, blocks, scale, causal, q_len, k_len, out, lse):
+        want = real(q[:4], k[:4], v[:4], blocks[:4], scale, causal, q_len[:4], k_len[:4], out[:4], lse[:4])
+        return [np.tile(t, (copies,) + (1,) * (t.ndim - 1)) for t in want]
+
+    monkeypatch.setattr(O, "block_attention", once)
+    q, k, v, blocks, kl = again(q), again(k), again(v), np.tile(blocks, (copies, 1, 1, 1)), kl * copies
+    got, lse = check_attention(q, k, v, blocks, q_len=kl, k_len=kl, clean=clean)
+    dev, n = torch.tensor(blocks, device="cuda"), torch.tensor(kl, dtype=torch.int32, device="cuda")
+    for _ in range(40):
+        o, z = qs.block_attention(q, k, v, dev, q_len=n, k_len=n, out=torch.full_like(got, 9.0), lse=torch.full_like(lse, 9.0))
+        assert torch.equal(o, got) and torch.equal(z, lse)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("dtype,D", [(BF16, 128), (F16, 64), (BF16, 64), (F16, 128)])
 @pytest.mark.parametrize("Lq,Lk,T", [(300, 300, 5), (300, 411, 7), (5, 900, 15), (64, 4096, 64)])
