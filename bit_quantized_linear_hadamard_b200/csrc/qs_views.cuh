@@ -54,11 +54,9 @@ struct Search {
     if (j == n) return other && from <= 0 && 0 <= to;
     if (--steps < 0) return true;
     const Term& t = term[j];
-    int64_t lo = t.lo, hi = t.hi;
-    if (t.stride > 0) {
-      lo = std::max(lo, -floor_div(most[j + 1] - from, t.stride));
-      hi = std::min(hi, floor_div(to - least[j + 1], t.stride));
-    }
+    if (t.stride == 0) return find(j + 1, from, to, true);  // any c_j, one that is not 0 among them
+    const int64_t lo = std::max(t.lo, -floor_div(most[j + 1] - from, t.stride));
+    const int64_t hi = std::min(t.hi, floor_div(to - least[j + 1], t.stride));
     for (int64_t c = lo; c <= hi; ++c) {
       if (find(j + 1, from - c * t.stride, to - c * t.stride, other || c != 0)) return true;
       if (steps < 0) return true;
